@@ -87,6 +87,15 @@ SIGNATURES = {
     "tts_quantize_fp8_weight": (_I, [_VP, _I, _I, _VP, _VP, _VP]),
     "tts_attention_decode": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _F, _VP]),
     "tts_attention_decode_noalloc": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _F, _VP]),
+    "tts_quantize_w4_weight": (_I, [_VP, _I, _I, _VP, _VP, _VP]),
+    "tts_gemv_w4": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _VP]),
+    "tts_quantize_kv4": (_I, [_VP, _VP, _I, _I, _I, _I, _VP, _VP, _VP, _VP, _I, _VP]),
+    "tts_dequantize_kv4": (_I, [_VP, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP, _I, _VP]),
+    "tts_attention_kv4_workspace": (_I, [_I, _I, ctypes.POINTER(ctypes.c_size_t)]),
+    "tts_attention_decode_kv4": (_I, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _F, _F, _VP,
+                                      ctypes.c_size_t, _VP]),
+    "tts_code_logprobs": (_I, [_VP, ctypes.c_longlong, _VP, _I, _I, _I, _F, _I, _VP, _VP, _VP, _VP, _VP]),
+    "tts_get_logprobs": (_I, [_VP, _VP, _F, _I, _VP, _VP, _VP, _VP]),
     "tts_status_str": (ctypes.c_char_p, [_I]),
 }
 
@@ -189,6 +198,125 @@ def attention_decode(qkv, q_norm, k_norm, k_cache, v_cache, out, n_q: int, n_kv:
     max_pos = k_cache.shape[-2]
     _call("tts_attention_decode", qkv.data_ptr(), q_norm.data_ptr(), k_norm.data_ptr(), k_cache.data_ptr(),
           v_cache.data_ptr(), out.data_ptr(), n_q, n_kv, max_pos, pos, eps, rope_theta, stream)
+
+
+# ----------------------------------------------------------------------------
+# 4-bit weights, 4-bit cache, scores of codes
+# ----------------------------------------------------------------------------
+
+def _check(fn: str, *wanted):
+    """Each of `wanted` is (tensor or None, element bytes, shape): raises
+    TtsError(TTS_ERR_ARG) unless the tensor is a contiguous CUDA tensor of that
+    element size and shape (its address and size are all the library sees)."""
+    for t, size, shape in wanted:
+        if t is not None and not (t.is_cuda and t.is_contiguous() and t.element_size() == size and t.shape == shape):
+            raise TtsError(fn, -1)
+
+
+def _opt(t):
+    return None if t is None else t.data_ptr()
+
+
+def quantize_w4_weight(w_dev, stream=None):
+    """tts_quantize_w4_weight on w_dev, bf16 (or int16 bf16 bits) [N][K]:
+    returns (uint8 [N][K/2], bfloat16 [N][K/128]) device tensors."""
+    torch = _torch()
+    N, K = w_dev.shape
+    _check("tts_quantize_w4_weight", (w_dev, 2, (N, K)))
+    q = torch.empty((N, K // 2), dtype=torch.uint8, device=w_dev.device)
+    s = torch.empty((N, K // 128), dtype=torch.bfloat16, device=w_dev.device)
+    _call("tts_quantize_w4_weight", w_dev.data_ptr(), N, K, q.data_ptr(), s.data_ptr(), stream)
+    return q, s
+
+
+def gemv_w4(x_dev, w4_dev, s_dev, y_dev, epi: int = 0, resid_dev=None, gamma_dev=None, eps: float = 1e-6,
+            stream=None) -> None:
+    """tts_gemv_w4: x_dev fp32 [M][K], w4_dev uint8 [N][K/2] and s_dev bf16
+    [N][K/128] (epi 2: 2N rows, gate then up), y_dev fp32 [M][N]; resid_dev
+    fp32 [M][N] for epi 1 (y_dev itself to add in place); gamma_dev bf16 [K]
+    normalises x."""
+    M, K = x_dev.shape
+    N = y_dev.shape[-1]
+    rows = 2 * N if epi == 2 else N
+    _check("tts_gemv_w4", (x_dev, 4, (M, K)), (w4_dev, 1, (rows, K // 2)), (s_dev, 2, (rows, K // 128)),
+           (y_dev, 4, (M, N)), (resid_dev, 4, (M, N)), (gamma_dev, 2, (K,)))
+    _call("tts_gemv_w4", x_dev.data_ptr(), w4_dev.data_ptr(), s_dev.data_ptr(), _opt(resid_dev), _opt(gamma_dev),
+          y_dev.data_ptr(), M, N, K, epi, eps, stream)
+
+
+def _check_kv4(fn: str, k4, v4, k_par, v_par):
+    n_kv, max_pos = k4.shape[0], k4.shape[1]
+    _check(fn, (k4, 1, (n_kv, max_pos, 64)), (v4, 1, (n_kv, max_pos, 64)), (k_par, 2, (n_kv, max_pos, 2, 2)),
+           (v_par, 2, (n_kv, max_pos, 2, 2)))
+    return n_kv, max_pos
+
+
+def quantize_kv4(k_dev, v_dev, k4, v4, k_par, v_par, p0: int, p1: int, stream=None) -> None:
+    """tts_quantize_kv4: positions [p0, p1) of bf16 caches [n_kv][stride][128]
+    into the 4-bit cache: k4, v4 uint8 [n_kv][max_pos][64], k_par, v_par bf16
+    [n_kv][max_pos][2][2]."""
+    n_kv, max_pos = _check_kv4("tts_quantize_kv4", k4, v4, k_par, v_par)
+    stride = k_dev.shape[1]
+    _check("tts_quantize_kv4", (k_dev, 2, (n_kv, stride, 128)), (v_dev, 2, (n_kv, stride, 128)))
+    _call("tts_quantize_kv4", k_dev.data_ptr(), v_dev.data_ptr(), n_kv, p0, p1, stride, k4.data_ptr(), v4.data_ptr(),
+          k_par.data_ptr(), v_par.data_ptr(), max_pos, stream)
+
+
+def dequantize_kv4(k4, v4, k_par, v_par, k_dev, v_dev, p0: int, p1: int, stream=None) -> None:
+    """tts_dequantize_kv4: the values of positions [p0, p1) of a 4-bit cache into
+    bf16 caches [n_kv][stride][128]."""
+    n_kv, max_pos = _check_kv4("tts_dequantize_kv4", k4, v4, k_par, v_par)
+    stride = k_dev.shape[1]
+    _check("tts_dequantize_kv4", (k_dev, 2, (n_kv, stride, 128)), (v_dev, 2, (n_kv, stride, 128)))
+    _call("tts_dequantize_kv4", k4.data_ptr(), v4.data_ptr(), k_par.data_ptr(), v_par.data_ptr(), n_kv, p0, p1,
+          max_pos, k_dev.data_ptr(), v_dev.data_ptr(), stride, stream)
+
+
+def kv4_workspace_bytes(n_q: int, n_kv: int) -> int:
+    """tts_attention_kv4_workspace: bytes of the zeroed scratch that
+    attention_decode_kv4 wants."""
+    n = ctypes.c_size_t()
+    _call("tts_attention_kv4_workspace", n_q, n_kv, ctypes.byref(n))
+    return n.value
+
+
+def attention_decode_kv4(qkv, q_norm, k_norm, k4, v4, k_par, v_par, out, n_q: int, n_kv: int, pos: int, workspace,
+                         kv_row=None, eps: float = 1e-6, rope_theta: float = 1e6, stream=None) -> None:
+    """tts_attention_decode_kv4 on torch device tensors: qkv fp32
+    [(n_q + 2 n_kv) 128], gains bf16 [128], the 4-bit cache as quantize_kv4
+    takes it, out fp32 [n_q 128], workspace a uint8 tensor of
+    kv4_workspace_bytes zeros (kept between calls), kv_row fp32 [2][n_kv][128]
+    or None."""
+    heads, max_pos = _check_kv4("tts_attention_decode_kv4", k4, v4, k_par, v_par)
+    _check("tts_attention_decode_kv4", (qkv, 4, ((n_q + 2 * n_kv) * 128,)), (q_norm, 2, (128,)), (k_norm, 2, (128,)),
+           (out, 4, (n_q * 128,)), (kv_row, 4, (2, n_kv, 128)), (workspace, 1, (workspace.numel(),)))
+    if heads != n_kv:
+        raise TtsError("tts_attention_decode_kv4", -1)
+    _call("tts_attention_decode_kv4", qkv.data_ptr(), q_norm.data_ptr(), k_norm.data_ptr(), k4.data_ptr(),
+          v4.data_ptr(), k_par.data_ptr(), v_par.data_ptr(), out.data_ptr(), _opt(kv_row), n_q, n_kv, max_pos, pos,
+          eps, rope_theta, workspace.data_ptr(), workspace.numel(), stream)
+
+
+def code_logprobs(logits, codes, cb_vocab: int, top: int = 0, temperature: float = 1.0, stream=None):
+    """tts_code_logprobs: logits fp32 [rows][ld] (rows may be strided) and codes
+    int32 [rows][n_cb]; returns (logprob [rows][n_cb], entropy [rows][n_cb],
+    top_codes [rows][n_cb][top], top_logprob [rows][n_cb][top])."""
+    torch = _torch()
+    rows, n_cb = codes.shape
+    _check("tts_code_logprobs", (codes, 4, (rows, n_cb)))
+    if not (logits.is_cuda and logits.dtype == torch.float32 and logits.dim() == 2 and logits.shape[0] == rows
+            and logits.shape[1] >= n_cb * cb_vocab and logits.stride(1) == 1):
+        raise TtsError("tts_code_logprobs", -1)
+    ld = logits.stride(0) if rows > 1 else logits.shape[1]
+    dev = logits.device
+    lp = torch.empty((rows, n_cb), dtype=torch.float32, device=dev)
+    ent = torch.empty((rows, n_cb), dtype=torch.float32, device=dev)
+    at = torch.empty((rows, n_cb, max(top, 0)), dtype=torch.int32, device=dev)
+    at_lp = torch.empty((rows, n_cb, max(top, 0)), dtype=torch.float32, device=dev)
+    _call("tts_code_logprobs", logits.data_ptr(), ld, codes.data_ptr(), rows, n_cb, cb_vocab, temperature, top,
+          lp.data_ptr(), ent.data_ptr(), at.data_ptr() if top > 0 else None, at_lp.data_ptr() if top > 0 else None,
+          stream)
+    return lp, ent, at, at_lp
 
 
 @dataclass
@@ -368,6 +496,18 @@ class Decoder:
         out = np.empty((self.dims.n_cb, self.dims.cb_vocab), np.float32)
         _call("tts_get_logits", self._ctx, _ptr(out))
         return out
+
+    def logprobs(self, codes=None, top: int = 0, temperature: float = 1.0):
+        """tts_get_logprobs on the last step's logits: (logprob [n_cb] of `codes`
+        (default: the codes the last step produced), entropy [n_cb], top codes
+        [n_cb][top], their log probabilities [n_cb][top])."""
+        n = self.dims.n_cb
+        lp, ent = np.empty(n, np.float32), np.empty(n, np.float32)
+        at, at_lp = np.empty((n, max(top, 0)), np.int32), np.empty((n, max(top, 0)), np.float32)
+        c = None if codes is None else np.ascontiguousarray(codes, np.int32).reshape(n)
+        _call("tts_get_logprobs", self._ctx, None if c is None else _ptr(c), float(temperature), top, _ptr(lp),
+              _ptr(ent), _ptr(at) if top > 0 else None, _ptr(at_lp) if top > 0 else None)
+        return lp, ent, at, at_lp
 
     def get_hidden(self) -> np.ndarray:
         out = np.empty(self.dims.hidden, np.float32)

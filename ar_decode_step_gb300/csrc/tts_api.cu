@@ -64,6 +64,7 @@ struct tts_ctx {
     float *part_o = nullptr, *part_ml = nullptr;
     unsigned* counters = nullptr;  // [n_kv] attention tickets, [n_kv] head ticket
     DevState* st = nullptr;
+    int* score = nullptr;  // tts_get_logprobs: codes in and results out (kScoreWords)
     int* hist = nullptr;
     int* prompt = nullptr;
 
@@ -96,6 +97,10 @@ struct tts_ctx {
 };
 
 namespace {
+
+// Words of tts_get_logprobs' scratch: codes, log probabilities and entropies
+// (one per codebook each), then the alternatives' codes and log probabilities.
+constexpr int kScoreWords = kMaxCodebooks * (3 + 2 * kMaxTop);
 
 int report(cudaError_t e, const char* what) {
     std::fprintf(stderr, "tts: %s failed: %s\n", what, cudaGetErrorString(e));
@@ -476,6 +481,7 @@ int init_impl(tts_ctx* c, const tts_config* cfg, const tts_weights* w) {
     TTS_TRY(dalloc(c, &c->part_ml, (size_t)k.n_kv_heads * c->S * c->G * 2));
     TTS_TRY(dalloc(c, &c->counters, (size_t)2 * k.n_kv_heads));
     TTS_TRY(dalloc(c, &c->st, 1));
+    TTS_TRY(dalloc(c, &c->score, kScoreWords));
     TTS_TRY(dalloc(c, &c->hist, (size_t)k.max_pos * k.n_codebooks));
     TTS_TRY(dalloc(c, &c->prompt, (size_t)k.max_pos * k.n_codebooks));
     TTS_CK(cudaMemsetAsync(c->kc, 0, kv * sizeof(__nv_bfloat16), c->stream));
@@ -980,6 +986,33 @@ int tts_get_logits(tts_ctx* ctx, float* out) {
     if (!out) return TTS_ERR_ARG;
     const size_t n = (size_t)ctx->cfg.n_codebooks * ctx->cfg.cb_vocab;
     TTS_CK(cudaMemcpyAsync(out, ctx->logits, n * sizeof(float), cudaMemcpyDeviceToHost, ctx->stream));
+    TTS_CK(cudaStreamSynchronize(ctx->stream));
+    return TTS_OK;
+}
+
+int tts_get_logprobs(tts_ctx* ctx, const int32_t* codes, float temperature, int top, float* logprob,
+                     float* entropy, int32_t* top_codes, float* top_logprob) {
+    if (!ctx) return TTS_ERR_STATE;
+    const int n_cb = ctx->cfg.n_codebooks, V = ctx->cfg.cb_vocab;
+    if (top < 0 || top > kMaxTop || top > V || (codes != nullptr && !logprob)) return TTS_ERR_ARG;
+    if ((top > 0) != (top_codes != nullptr) || (top > 0) != (top_logprob != nullptr)) return TTS_ERR_ARG;
+    for (int k = 0; codes && k < n_cb; ++k)
+        if (codes[k] < 0 || codes[k] >= V) return TTS_ERR_CODE;
+    float* f = reinterpret_cast<float*>(ctx->score);
+    float *d_lp = f + kMaxCodebooks, *d_ent = f + 2 * kMaxCodebooks, *d_top_lp = f + kMaxCodebooks * (3 + kMaxTop);
+    int* d_top = ctx->score + 3 * kMaxCodebooks;
+    if (codes)
+        TTS_CK(cudaMemcpyAsync(ctx->score, codes, n_cb * sizeof(int), cudaMemcpyHostToDevice, ctx->stream));
+    TTS_TRY(tts_code_logprobs(ctx->logits, (long long)n_cb * V, logprob ? (codes ? ctx->score : ctx->st->codes) : nullptr,
+                              1, n_cb, V, temperature, top, logprob ? d_lp : nullptr, entropy ? d_ent : nullptr,
+                              top ? d_top : nullptr, top ? d_top_lp : nullptr, ctx->stream));
+    auto back = [&](void* dst, const void* src, int words) {
+        return dst ? cudaMemcpyAsync(dst, src, words * sizeof(int), cudaMemcpyDeviceToHost, ctx->stream) : cudaSuccess;
+    };
+    TTS_CK(back(logprob, d_lp, n_cb));
+    TTS_CK(back(entropy, d_ent, n_cb));
+    TTS_CK(back(top_codes, d_top, n_cb * top));
+    TTS_CK(back(top_logprob, d_top_lp, n_cb * top));
     TTS_CK(cudaStreamSynchronize(ctx->stream));
     return TTS_OK;
 }

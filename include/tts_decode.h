@@ -232,6 +232,18 @@ int tts_get_kv(tts_ctx* ctx, void* k_host, void* v_host, int p0, int p1);
 /* HOST fp32 [n_codebooks*cb_vocab]: the logits of the last decode step. */
 int tts_get_logits(tts_ctx* ctx, float* logits_host);
 
+/* The last decode step's logits as tts_code_logprobs reads them (one row):
+ * per codebook the log probability of a given code, the entropy, and the `top`
+ * most probable codes.  codes: HOST int32 [n_codebooks] (TTS_ERR_CODE when one
+ * is outside [0, cb_vocab)), or NULL for the codes that the next step embeds
+ * (those the last step produced, after the delay mask).  logprob, entropy:
+ * HOST fp32 [n_codebooks]; top_codes HOST int32, top_logprob HOST fp32
+ * [n_codebooks][top]; logprob (without codes) and entropy may be NULL,
+ * top_codes and top_logprob are NULL exactly when top is 0.  Arguments and
+ * errors as tts_code_logprobs.  Synchronises the stream. */
+int tts_get_logprobs(tts_ctx* ctx, const int32_t* codes, float temperature, int top, float* logprob, float* entropy,
+                     int32_t* top_codes, float* top_logprob);
+
 /* HOST fp32 [hidden]: the residual stream after the last layer of the last
  * decode step (the input of the final RMSNorm), or of the last prompt row
  * of a position-by-position prefill; the batched prefill leaves it as it
@@ -369,6 +381,104 @@ int tts_gemm_tiled(const void* A, const void* B, const float* a_scale, const flo
  * W: DEVICE bf16 [N][K]; W8: DEVICE uint8 [N][K]; s: DEVICE fp32 [N].
  * stream: cudaStream_t or NULL.  Asynchronous. */
 int tts_quantize_fp8_weight(const void* W, int N, int K, void* W8, float* s, void* stream);
+
+/* 4-bit weights with group scales.  W4: DEVICE uint8 [N][K/2], the low nibble
+ * of a byte holding the even k; s: DEVICE bf16 [N][K/128], one scale per row
+ * and 128 consecutive k; a weight is s * (u - 8) for its nibble u.
+ * tts_quantize_w4_weight makes them from W, DEVICE bf16 [N][K]: per group
+ * s = bf16(max |w| / 7), u = 8 + clamp(rint(w / s), -8, 7) (IEEE fp32
+ * divisions, rounding to nearest even; u = 8 where s is 0).  W finite.
+ * K % 128 == 0; W and W4 16-byte aligned.  Enqueued on `stream` (NULL: the
+ * default stream); does not synchronise.  TTS_ERR_ARG for bad sizes, NULL or
+ * misaligned pointers. */
+int tts_quantize_w4_weight(const void* W, int N, int K, void* W4, void* s, void* stream);
+
+/* Stand-alone op: the matrix-vector products of a decode step over 4-bit
+ * weights, for one activation vector or a few (short prompts, candidates).
+ *   x: DEVICE fp32 [M][K]; W4, s: the weights above, N rows (epi 2: 2N, gate
+ *   rows then up rows); a = x, or with gamma (DEVICE bf16 [K], may be NULL)
+ *   the RMSNorm a = x / sqrt(mean(x^2) + eps) * gamma.
+ *   epi 0: y = a . W^T; epi 1: y = resid + a . W^T; epi 2: SwiGLU,
+ *   y = silu(a . gate^T) * (a . up^T).  y: DEVICE fp32 [M][N]; resid: DEVICE
+ *   fp32 [M][N] for epi 1 (may be y itself), NULL otherwise.
+ * Activations stay fp32 (no rounding to 16 bits), sums are fp32, and every
+ * result is deterministic.  1 <= M <= 8, K % 128 == 0, 128 <= K <= 12288, any
+ * N from 1 to 2^24.  x, W4 and gamma 16-byte aligned; y overlaps no input
+ * (but resid == y).  Enqueued on `stream` (NULL: the default stream); does
+ * not synchronise; may be captured.  TTS_ERR_ARG otherwise. */
+int tts_gemv_w4(const float* x, const void* W4, const void* s, const float* resid, const void* gamma, float* y, int M,
+                int N, int K, int epi, float eps, void* stream);
+
+/* A key-value cache held in 4 bits, one layer of it: k4, v4: DEVICE uint8
+ * [n_kv][max_pos][64]; k_par, v_par: DEVICE bf16 [n_kv][max_pos][2][2].  A row
+ * of 128 channels has two halves, 0-63 and 64-127, each with a (scale,
+ * minimum) pair; the channel with nibble u has the value minimum + scale * u.
+ * Byte 8r + j of a row holds channels 8r + 2j (low nibble) and 8r + 2j + 1 for
+ * j < 4, and the same channels + 64 in byte 8r + 4 + j.  72 bytes a row
+ * against 256 in bf16.
+ * tts_quantize_kv4 writes positions [p0, p1) from bf16 caches k, v: DEVICE
+ * [n_kv][src_stride][128] (position p is row p of each head, as in
+ * tts_set_kv): per half minimum = min x, scale = bf16((max x - min x) / 15),
+ * u = clamp(rint((x - minimum) / scale), 0, 15) (IEEE fp32 operations; u = 0
+ * where the scale is 0).  A half that holds a NaN or an infinity, or whose
+ * range overflows, reads back as NaN.  tts_dequantize_kv4 writes the values of
+ * positions [p0, p1), rounded to bf16, into bf16 caches of dst_stride
+ * positions a head.  Rows outside [p0, p1) are left as they are; p0 == p1
+ * does nothing.  All pointers 16-byte aligned, 1 <= max_pos <= 2^20.
+ * Enqueued on `stream` (NULL: the default stream); neither synchronises.
+ * TTS_ERR_FULL if p1 > max_pos; TTS_ERR_ARG if p1 exceeds the bf16 cache's
+ * stride, for bad sizes, NULL or misaligned pointers. */
+int tts_quantize_kv4(const void* k, const void* v, int n_kv, int p0, int p1, int src_stride, void* k4, void* v4,
+                     void* k_par, void* v_par, int max_pos, void* stream);
+int tts_dequantize_kv4(const void* k4, const void* v4, const void* k_par, const void* v_par, int n_kv, int p0, int p1,
+                       int max_pos, void* k, void* v, int dst_stride, void* stream);
+
+/* tts_attention_decode over a 4-bit cache: for position pos the query and key
+ * heads are RMS-normalised and rotated as there, the key and value rows of pos
+ * are rounded to bf16, quantised as tts_quantize_kv4 does and written to the
+ * cache, and the n_q query heads attend positions [0, pos], every key and
+ * value (those of pos too) as the cache holds it.  qkv, q_norm, k_norm, out,
+ * head counts as tts_attention_decode; max_pos up to 2^20, n_q up to 4096.
+ * Scores, softmax and sums are fp32, the new key is computed in fp64 up to
+ * its rounding (its codes do not depend on the order of a sum), and every
+ * result is deterministic.  kv_row: DEVICE fp32 [2][n_kv][128], the key and
+ * value of pos as the cache now holds them, or NULL.
+ * workspace: DEVICE, at least tts_attention_kv4_workspace bytes, 16-byte
+ * aligned, zeroed once by the caller before its first use; every call leaves
+ * it ready for the next one.  Calls that may overlap on the GPU (other
+ * streams, other captured graphs) need a workspace each; calls ordered on one
+ * stream share one.  Enqueued on `stream` (NULL: the default stream); does not
+ * synchronise; may be captured (a replay repeats position pos).
+ * TTS_ERR_FULL if pos >= max_pos; TTS_ERR_ARG for bad sizes, a short
+ * workspace, NULL or misaligned (16 bytes) pointers. */
+int tts_attention_kv4_workspace(int n_q, int n_kv, size_t* bytes);
+int tts_attention_decode_kv4(const float* qkv, const void* q_norm, const void* k_norm, void* k4, void* v4, void* k_par,
+                             void* v_par, float* out, float* kv_row, int n_q, int n_kv, int max_pos, int pos,
+                             float eps, float rope_theta, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Log probabilities of given codes under the head's logits (scoring of a
+ * teacher-forced utterance, confidence of a sampled one).  logits: DEVICE
+ * fp32, row r's codebook k at logits + r * ld + k * cb_vocab, ld >= n_cb *
+ * cb_vocab; with p = softmax(logits / temperature) over a codebook's cb_vocab
+ * entries:
+ *   logprob [rows][n_cb] = log p[codes[r][k]] (codes: DEVICE int32
+ *   [rows][n_cb]; both NULL: not computed; a code outside [0, cb_vocab) gives
+ *   NaN);
+ *   entropy [rows][n_cb] = -sum p log p, in nats (may be NULL);
+ *   top_codes, top_logprob [rows][n_cb][top]: the `top` entries with the
+ *   largest logits, largest first, equal logits by the lower code (NULL
+ *   exactly when top is 0).
+ * Entries of -inf (masked) have probability 0 and no share in the entropy; a
+ * codebook with nothing but -inf has log probabilities -inf and entropy 0.
+ * With a NaN or +inf among its logits a codebook's log probabilities and
+ * entropy are NaN; NaN entries rank last.  DEVICE outputs, fp32 and int32.
+ * 0 <= rows, 1 <= n_cb <= 8, 2 <= cb_vocab <= 2^20, 0 <= top <= min(32,
+ * cb_vocab), temperature positive and finite.  Pointers 4-byte aligned.
+ * Enqueued on `stream` (NULL: the default stream); does not synchronise; may
+ * be captured.  TTS_ERR_ARG otherwise. */
+int tts_code_logprobs(const float* logits, long long ld, const int32_t* codes, int rows, int n_cb, int cb_vocab,
+                      float temperature, int top, float* logprob, float* entropy, int32_t* top_codes,
+                      float* top_logprob, void* stream);
 
 /* One layer's decode attention as a standalone call, outside a context: the
  * kernel the step uses ("Higgs Audio v3 TTS-4B on FlashRT", section 5: fused
