@@ -424,7 +424,8 @@ int tts_gemv_w4(const float* x, const void* W4, const void* s, const float* resi
  * range overflows, reads back as NaN.  tts_dequantize_kv4 writes the values of
  * positions [p0, p1), rounded to bf16, into bf16 caches of dst_stride
  * positions a head.  Rows outside [p0, p1) are left as they are; p0 == p1
- * does nothing.  All pointers 16-byte aligned, 1 <= max_pos <= 2^20.
+ * does nothing.  All pointers 16-byte aligned, 1 <= max_pos <= 2^20,
+ * n_kv up to 1024.
  * Enqueued on `stream` (NULL: the default stream); neither synchronises.
  * TTS_ERR_FULL if p1 > max_pos; TTS_ERR_ARG if p1 exceeds the bf16 cache's
  * stride, for bad sizes, NULL or misaligned pointers. */
@@ -438,7 +439,8 @@ int tts_dequantize_kv4(const void* k4, const void* v4, const void* k_par, const 
  * are rounded to bf16, quantised as tts_quantize_kv4 does and written to the
  * cache, and the n_q query heads attend positions [0, pos], every key and
  * value (those of pos too) as the cache holds it.  qkv, q_norm, k_norm, out,
- * head counts as tts_attention_decode; max_pos up to 2^20, n_q up to 4096.
+ * head counts as tts_attention_decode; max_pos up to 2^20, n_q up to 4096,
+ * n_kv up to 1024.
  * Scores, softmax and sums are fp32, the new key is computed in fp64 up to
  * its rounding (its codes do not depend on the order of a sum), and every
  * result is deterministic.  kv_row: DEVICE fp32 [2][n_kv][128], the key and
@@ -447,7 +449,7 @@ int tts_dequantize_kv4(const void* k4, const void* v4, const void* k_par, const 
  * aligned, zeroed once by the caller before its first use; every call leaves
  * it ready for the next one.  Calls that may overlap on the GPU (other
  * streams, other captured graphs) need a workspace each; calls ordered on one
- * stream share one.  Enqueued on `stream` (NULL: the default stream); does not
+ * stream share one, of any shapes.  Enqueued on `stream` (NULL: the default stream); does not
  * synchronise; may be captured (a replay repeats position pos).
  * TTS_ERR_FULL if pos >= max_pos; TTS_ERR_ARG for bad sizes, a short
  * workspace, NULL or misaligned (16 bytes) pointers. */
