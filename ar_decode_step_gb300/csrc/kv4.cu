@@ -29,16 +29,6 @@ constexpr size_t kTicketBytes = 4 * kKv4MaxKvHeads;  // the workspace's first by
 struct RopeRow {
     float2 cs[kHeadDim / 2], rest[kHeadDim / 2];
 };
-__device__ __forceinline__ void rope_at(const RopeRow& r, int i, float* c, float* s) {
-    const float2 v = r.cs[i];
-    *c = v.x;
-    *s = v.y;
-}
-__device__ __forceinline__ void rope_at(const RopeRow& r, int i, double* c, double* s) {
-    const float2 v = r.cs[i], d = r.rest[i];
-    *c = (double)v.x + (double)d.x;
-    *s = (double)v.y + (double)d.y;
-}
 
 struct Kv4Params {
     const float* qkv;
@@ -56,31 +46,37 @@ struct Kv4Params {
     RopeRow rope;
 };
 
+// fp32 bits in the order of the values, as a signed integer, and back.
+__device__ __forceinline__ int ordered(float x) {
+    const int b = __float_as_int(x);
+    return b ^ ((b >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float from_ordered(int b) { return __int_as_float(b ^ ((b >> 31) & 0x7fffffff)); }
+
 // Quantise one row held by a warp: lane l has channels 4l .. 4l + 3 (bf16
 // values), so lanes 0-15 hold half 0 and lanes 16-31 half 1.  Returns the
 // lane's four codes in 16 bits; *par is its half's parameter word.  The
 // arithmetic is IEEE fp32 as defined above.  A half whose range is not finite
 // (it holds a NaN or an infinity) gets NaN parameters: its values read as NaN.
 __device__ __forceinline__ uint32_t quant_row(const float x[4], uint32_t* par) {
-    float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
-    float hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-    int bad = !(isfinite(x[0]) && isfinite(x[1]) && isfinite(x[2]) && isfinite(x[3]));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-    }
+    const unsigned half = (threadIdx.x & 16) ? 0xffff0000u : 0x0000ffffu;
+    const int lo4 = min(min(ordered(x[0]), ordered(x[1])), min(ordered(x[2]), ordered(x[3])));
+    const int hi4 = max(max(ordered(x[0]), ordered(x[1])), max(ordered(x[2]), ordered(x[3])));
+    // + 0: a minimum of -0 is stored as 0.  NaN and infinities sort to the ends
+    const float lo = from_ordered(__reduce_min_sync(half, lo4)) + 0.f, hi = from_ordered(__reduce_max_sync(half, hi4));
     const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(hi - lo, 15.f));
     const float s = __bfloat162float(sb);
-    if (bad || !isfinite(s)) {
+    if (!isfinite(s)) {
         *par = 0x7fff7fffu;
         return 0;
     }
+    // quotients by one reciprocal; below 2^-60 numerator and divisor are scaled
+    // so that the reciprocal stays finite
+    const float k = s < 0x1p-60f ? 0x1p100f : 1.f, ks = s * k, rs = __frcp_rn(ks);
     uint32_t code = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float q = s > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x[j] - lo, s)), 0.f), 15.f) : 0.f;
+        const float q = s > 0.f ? fminf(fmaxf(rintf(div_rn_by((x[j] - lo) * k, ks, rs)), 0.f), 15.f) : 0.f;
         code |= (uint32_t)q << (4 * j);
     }
     *par = (uint32_t)__bfloat16_as_ushort(sb) | (__float_as_uint(lo) & 0xffff0000u);
@@ -136,29 +132,70 @@ __global__ void __launch_bounds__(256) dequantize_kv4_kernel(const uint8_t* k4, 
     for (int j = 0; j < 4; ++j) dst[j] = __bfloat16_as_ushort(__float2bfloat16_rn(x[j]));
 }
 
-// q/k RMSNorm over the head then rotate-half RoPE, in type T: lane l has
-// channels 4l .. 4l + 3, whose rotation partners sit in lane l ^ 16.
-template <typename T>
-__device__ __forceinline__ void norm_rope(const float* src, const __nv_bfloat16* gain, const RopeRow& rope, float eps,
-                                          int lane, T o[4]) {
-    T a[4], ss = 0;
+// q/k RMSNorm over the head then rotate-half RoPE: lane l has channels
+// 4l .. 4l + 3, whose rotation partners sit in lane l ^ 16.
+__device__ __forceinline__ void norm_rope(float4 x, uint2 gb, const float4* rope, float eps, int lane, float o[4]) {
+    const float ss = warp_sum(x.x * x.x + x.y * x.y + x.z * x.z + x.w * x.w);
+    const float r = 1.0f / sqrtf(ss / (float)kHeadDim + eps);
+    const float a[4] = {x.x * r * bf16lo(gb.x), x.y * r * bf16hi(gb.x), x.z * r * bf16lo(gb.y), x.w * r * bf16hi(gb.y)};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        a[j] = (T)src[4 * lane + j];
-        ss += a[j] * a[j];
+        const float partner = __shfl_xor_sync(0xffffffffu, a[j], 16);
+        const float4 cs = rope[(4 * lane + j) & 63];
+        o[j] = lane < 16 ? a[j] * cs.x - partner * cs.y : a[j] * cs.x + partner * cs.y;
     }
+}
+
+// The same to about 2^-44, for the new key: its 4-bit codes are a step
+// function of it and must not depend on the order of an fp32 sum.  Numbers are
+// unevaluated sums hi + lo of two fp32 (Dekker's and Knuth's error-free
+// product and sum); the fp64 unit took 6 us for these 128 channels.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two two_prod(float a, float b) {
+    const float p = __fmul_rn(a, b);
+    return {p, __fmaf_rn(a, b, -p)};
+}
+__device__ __forceinline__ Two renorm(float hi, float lo) {
+    const float s = __fadd_rn(hi, lo);
+    return {s, __fsub_rn(lo, __fsub_rn(s, hi))};
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+    const Two s = two_sum(a.hi, b.hi);
+    return renorm(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+    const Two p = two_prod(a.hi, b.hi);
+    return renorm(p.hi, __fadd_rn(p.lo, __fmaf_rn(a.hi, b.lo, __fmul_rn(a.lo, b.hi))));
+}
+__device__ __forceinline__ void norm_rope_exact(float4 x4, uint2 gb, const float4* rope, float eps, int lane,
+                                                float o[4]) {
+    const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+    const float gn[4] = {bf16lo(gb.x), bf16hi(gb.x), bf16lo(gb.y), bf16hi(gb.y)};
+    Two ss = add(add(two_prod(x[0], x[0]), two_prod(x[1], x[1])), add(two_prod(x[2], x[2]), two_prod(x[3], x[3])));
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-    const T r = (T)1 / sqrt(ss / (T)kHeadDim + (T)eps);
+    for (int d = 16; d > 0; d >>= 1)
+        ss = add(ss, Two{__shfl_xor_sync(0xffffffffu, ss.hi, d), __shfl_xor_sync(0xffffffffu, ss.lo, d)});
+    const Two v = add(Two{ss.hi * (1.f / kHeadDim), ss.lo * (1.f / kHeadDim)}, Two{eps, 0.f});
+    // 1 / sqrt(v): an fp32 value y corrected by Newton's step on e = 1 - v y^2
+    const float y = 1.0f / sqrtf(v.hi);
+    const Two vy2 = mul(v, two_prod(y, y));
+    const float e = __fsub_rn(__fsub_rn(1.f, vy2.hi), vy2.lo);
+    const Two rs{y, y * e * (0.5f + 0.375f * e)};
+    Two a[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) a[j] = a[j] * r * (T)__bfloat162float(gain[4 * lane + j]);
+    for (int j = 0; j < 4; ++j) a[j] = mul(two_prod(x[j], gn[j]), rs);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const T partner = __shfl_xor_sync(0xffffffffu, a[j], 16);
-        const int i = (4 * lane + j) & 63;
-        T c, s;
-        rope_at(rope, i, &c, &s);
-        o[j] = lane < 16 ? a[j] * c - partner * s : a[j] * c + partner * s;
+        const Two partner{__shfl_xor_sync(0xffffffffu, a[j].hi, 16), __shfl_xor_sync(0xffffffffu, a[j].lo, 16)};
+        const float4 cs = rope[(4 * lane + j) & 63];
+        const float sg = lane < 16 ? -1.f : 1.f;
+        o[j] = add(mul(a[j], Two{cs.x, cs.z}), mul(partner, Two{sg * cs.y, sg * cs.w})).hi;
     }
 }
 
@@ -170,27 +207,28 @@ __device__ __forceinline__ void norm_rope(const float* src, const __nv_bfloat16*
 //
 // Both products run on the tensor cores (m16n8k16, fp16 operands, fp32 sums),
 // with the codes as they lie in memory: a nibble masked out of its 16-bit half
-// IS the fp16 subnormal u 2^-24 (or, from bits 4-7, 16 u 2^-24), exact, so a
-// code costs 5/8 of an instruction and no conversion.  The powers of two and
-// the factor 16 are taken back on the other operand or in the epilogue.
-//   scores  A = queries (rows 0-7: the group's heads, fp16 high parts; rows
-//           8-15: their low parts), B = K codes.  score = sum over halves of
-//           s_K (q . u) + m_K sum(q): the scale and the minimum of a position
-//           enter in fp32 on the accumulators.
-//   output  A = weights p s_V of each position, again high and low parts in
-//           rows r and r + 8, B = V codes; sum of p m_V beside it in fp32.
-// Two fp16 parts of a value scaled by a power of two to below 2^15 keep 22
-// bits (and 2^-39 of the row's largest), so nothing falls under fp32 accuracy
-// by more than rounding of the sums.  The scaling of the weights follows their
-// running maximum per head and half, like the softmax maximum.
-//
-// Column n of block b of a tile's 16 positions is position
-// 4 (n / 2) + 2 b + n % 2: an accumulator's two columns and the two blocks of
-// a lane are then four neighbouring positions, the ones whose V rows the lane
-// reads, and the score accumulators are the weight operand without a shuffle.
-constexpr int kAttnWarps = 12;
+// IS the fp16 subnormal u 2^-24, and a byte of two nibbles (u + 16 u') 2^-24,
+// exact, so a code costs about half an instruction and no conversion.  The
+// powers of two are taken back, and the even nibble out of the byte, on the
+// other operand or in the epilogue.
+//   scores  A = K codes (16 positions), B = queries.  score = sum over halves
+//           of s_K (q . u) + m_K sum(q): the scale and the minimum of a
+//           position enter in fp32 on the accumulators.
+//   output  A = V codes (16 channels of a half), B = p s_V of 16 positions;
+//           sum of p m_V beside it in fp32.
+// The other operand is fp32 in two fp16 parts, of a value scaled by a power of
+// two towards fp16's upper end: 22 bits, and for small ones a floor of 2^-39
+// (queries) or 2^-33 (weights) of the largest, so nothing falls below fp32
+// accuracy by more than the rounding of the sums.  Up to four query
+// heads sit side by side with their low parts in the product's eight columns;
+// eight heads take a product for each part.  The scaling of the weights
+// follows their running maximum per head and half, like the softmax maximum.
+// (Queries and weights as A, codes as B was measured first: the same integer
+// work, but 32 products a tile instead of 16 and 96 registers of operands and
+// sums instead of 48, so 12 warps an SM instead of 16.)
+constexpr int kAttnWarps = 16;
 constexpr int kTilePos = 16;
-constexpr int kStages = 6;
+constexpr int kStages = 4;
 constexpr int kStageV = kTilePos * kRowBytes;             // K rows, then V rows (permuted)
 constexpr int kStagePar = 2 * kStageV;                    // then K and V parameters
 constexpr int kStageBytes = kStagePar + 2 * kTilePos * 8;
@@ -198,6 +236,9 @@ constexpr int kRingBytes = kStages * kStageBytes;         // per warp
 constexpr int kAttnSmem = kAttnWarps * kRingBytes;
 static_assert(kRingBytes >= 8 * kHeadDim * 4, "a warp's output partial reuses its ring");
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -208,10 +249,16 @@ __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commi
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-__device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma16816(float c[4], const uint32_t a[4], uint2 b) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+}
+// c = A B, without clearing c first
+__device__ __forceinline__ void mma16816_first(float c[4], const uint32_t a[4], uint2 b) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "f"(0.f));
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -226,44 +273,90 @@ __device__ __forceinline__ void split_h2(float x, float y, uint32_t* hi, uint32_
     *hi = *reinterpret_cast<const uint32_t*>(&h);
     *lo = *reinterpret_cast<const uint32_t*>(&r);
 }
+// Bytes 0 and 2 (s = 0) or 1 and 3 of w, each in the low byte of a 16-bit half.
+__device__ __forceinline__ uint32_t bytes(uint32_t w, int s) {
+    return s ? __byte_perm(w, 0u, 0x4341u) : w & 0x00ff00ffu;
+}
+// The transpose of an 8 x 8 matrix of 16-bit values held by a warp, lane
+// (row, pair of columns).
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
 // The biased exponent of w >= 0, at least 14, and the power of two that takes
 // w to [2^14, 2^15).
 __device__ __forceinline__ int expo(float w) { return max((int)(__float_as_uint(w) >> 23), 14); }
 __device__ __forceinline__ float pow2_field(int field) { return __uint_as_float((uint32_t)field << 23); }
 __device__ __forceinline__ float to_2p15(int e) { return pow2_field(268 - e); }
+// For the weights, to [2^8, 2^9): six more doublings fit before fp16 ends, so
+// that a weight above all before it seldom moves the scale (measured: with
+// none to spare every second tile of normal data did), and the floor of the
+// low parts is still 2^-33 of the largest weight.
+__device__ __forceinline__ float to_2p9(int e) { return pow2_field(262 - e); }
+__device__ __forceinline__ int expo_of(float to) { return 262 - (int)(__float_as_uint(to) >> 23); }
 
-// Copies of one tile into a stage: codes of both caches and their parameters;
-// rows at and past `n` read as zero and are not touched in memory.
-struct TileSrc {
-    const uint8_t *k, *v, *kp, *vp;  // the head's row 0
+// A lane's share of a tile's copies: codes of both caches (two 16-byte pieces
+// each) and one row's 8 parameter bytes (a head's parameters start on 8 bytes
+// only when max_pos is odd; lanes 0-15 K, 16-31 V).  Rows at and past n read
+// as zero and are not touched in memory.
+struct LaneCopy {
+    const uint8_t *k, *v, *par;  // at tile 0
+    uint32_t k_dst, v_dst[2], par_dst;
     int n;
-};
-__device__ __forceinline__ void issue_tile(const TileSrc& s, int tile, uint32_t stage, int lane) {
-    const int row0 = tile * kTilePos;
+    __device__ __forceinline__ LaneCopy(const Kv4Params& p, size_t base, uint32_t ring, int lane) {
+        k = p.k4 + base * kRowBytes + lane * 16;
+        v = p.v4 + base * kRowBytes + lane * 16;
+        par = reinterpret_cast<const uint8_t*>((lane < 16 ? p.k_par : p.v_par) + (base + (lane & 15)) * 2);
+        n = p.pos;
+        k_dst = ring + lane * 16;
+        // V: rows 2 t + (0, 1, 8, 9) at column pair t of four lines, so that the
+        // 8-byte reads of the output product touch every bank once
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int idx = lane + 32 * i, row = idx >> 2, c = idx & 3;
-        const int bytes = row0 + row < s.n ? 16 : 0;
-        const size_t off = bytes ? (size_t)(row0 + row) * kRowBytes + c * 16 : 0;
-        cp_async16_zfill(stage + idx * 16, s.k + off, bytes);
-        // V: the four rows of a lane in one 128-byte line position each, so
-        // that the 8-byte reads below touch every bank once
-        const int line = (row & 3) * 2 + (c >> 1), slot = 2 * (row >> 2) + (c & 1);
-        cp_async16_zfill(stage + kStageV + line * 128 + slot * 16, s.v + off, bytes);
+        for (int i = 0; i < 2; ++i) {
+            const int idx = lane + 32 * i, row = idx >> 2, c = idx & 3;
+            const int line = ((row & 1) + 2 * (row >> 3)) * 2 + (c >> 1), slot = 2 * ((row >> 1) & 3) + (c & 1);
+            v_dst[i] = ring + kStageV + line * 128 + slot * 16;
+        }
+        par_dst = ring + kStagePar + lane * 8;
     }
-    // one row's 8 bytes a lane (a head's parameters start on 8 bytes only when
-    // max_pos is odd): lanes 0-15 K, 16-31 V
-    const int row = row0 + (lane & 15), bytes = row < s.n ? 8 : 0;
-    cp_async8_zfill(stage + kStagePar + lane * 8, (lane < 16 ? s.kp : s.vp) + (bytes ? (size_t)row * 8 : 0), bytes);
-}
+    __device__ __forceinline__ void issue(int tile, int stage, int lane) const {
+        const size_t off = (size_t)tile * (kTilePos * kRowBytes);
+        const uint32_t s = stage * kStageBytes;
+        const int left = n - tile * kTilePos;
+        if (left >= kTilePos) {
+            cp_async16(k_dst + s, k + off);
+            cp_async16(k_dst + s + 512, k + off + 512);
+            cp_async16(v_dst[0] + s, v + off);
+            cp_async16(v_dst[1] + s, v + off + 512);
+            cp_async8_zfill(par_dst + s, par + (size_t)tile * (kTilePos * 8), 8);
+        } else {
+            const int b0 = (lane >> 2) < left ? 16 : 0, b1 = (lane >> 2) + 8 < left ? 16 : 0;
+            const int bp = (lane & 15) < left ? 8 : 0;
+            // a copy of no bytes still wants an address inside the cache: row 0's
+            const uint8_t *k0 = b0 ? k + off : k - lane * 16, *k1 = b1 ? k + off + 512 : k - lane * 16;
+            const uint8_t *v0 = b0 ? v + off : v - lane * 16, *v1 = b1 ? v + off + 512 : v - lane * 16;
+            cp_async16_zfill(k_dst + s, k0, b0);
+            cp_async16_zfill(k_dst + s + 512, k1, b1);
+            cp_async16_zfill(v_dst[0] + s, v0, b0);
+            cp_async16_zfill(v_dst[1] + s, v1, b1);
+            cp_async8_zfill(par_dst + s, bp ? par + (size_t)tile * (kTilePos * 8) : par - (lane & 15) * 8, bp);
+        }
+    }
+};
 
 template <int G>
 __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __grid_constant__ Kv4Params p) {
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ float qs[G][kHeadDim];               // log2(e) / sqrt(128) times the rotated queries
-    __shared__ float knew[kHeadDim], vnew[kHeadDim];  // the new row as cached
+    __shared__ float4 rope[kHeadDim / 2];             // (cos, sin, rest of cos, rest of sin)
+    __shared__ __align__(16) float qs[G][kHeadDim];   // log2(e) / sqrt(128) times the rotated queries
+    constexpr bool kPack = G <= 4;      // high and low parts in one product's columns
+    constexpr int kParts = kPack ? 1 : 2;
+    __shared__ uint2 frag[kParts][4][2][32];          // the scores' query operand, by lane
+    __shared__ float qhead[G][3];                     // sums over the halves, 2^24 over the operand's power of two
+    __shared__ __align__(16) float vnew[kHeadDim];    // the new value row as cached
     __shared__ float wm[kAttnWarps + 1][G], wl[kAttnWarps + 1][G];
-    __shared__ float merge_c[kMaxSplitUnits][G];
+    __shared__ float merge_c[kMaxSplitUnits][G];      // a partial's weight in the merge
     __shared__ float merge_l[G];
     __shared__ int s_last;
 
@@ -274,228 +367,323 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
     const size_t base = (size_t)g * p.max_pos;
     const int tile_end = min((p.pos + kTilePos - 1) / kTilePos, (split + 1) * p.tiles_per_split);
 
-    const TileSrc src{p.k4 + base * kRowBytes, p.v4 + base * kRowBytes, reinterpret_cast<const uint8_t*>(p.k_par + base * 2),
-                      reinterpret_cast<const uint8_t*>(p.v_par + base * 2), p.pos};
+    // the group's queries, one warp each, and in the last split the new row, its
+    // key by the last warp and its value by the one before: their loads first
+    const bool new_k = has_new && warp == kAttnWarps - 1, new_v = has_new && warp == kAttnWarps - 2;
+    float4 x = {};
+    uint2 gain = {};
+    if (warp < G || new_k || new_v) {
+        const int vec = new_v ? p.n_q + p.n_kv + g : new_k ? p.n_q + g : g * G + warp;
+        x = reinterpret_cast<const float4*>(p.qkv)[(size_t)vec * (kHeadDim / 4) + lane];
+        gain = reinterpret_cast<const uint2*>(new_k ? p.k_norm : p.q_norm)[lane];
+    }
     uint8_t* my_ring = ring + warp * kRingBytes;
-    const uint32_t my_ring_s = smem_u32(my_ring);
+    const LaneCopy copy(p, base, smem_u32(my_ring), lane);
     int next = split * p.tiles_per_split + warp;  // next tile to copy
+    if (next < tile_end) copy.issue(next, 0, lane);
+    cp_async_commit();
+    next += kAttnWarps;
+    // the angles from the launch parameters to shared memory, an entry a warp at
+    // a time: parameters are read fast at one address a warp only
+    constexpr int kEach = (kHeadDim / 2 + kAttnWarps - 1) / kAttnWarps;
+    float2 cs[kEach], rest[kEach];
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-        if (next < tile_end) issue_tile(src, next, my_ring_s + s * kStageBytes, lane);
+    for (int i = 0; i < kEach; ++i) {
+        const int at = min(warp + i * kAttnWarps, kHeadDim / 2 - 1);
+        cs[i] = p.rope.cs[at];
+        rest[i] = p.rope.rest[at];
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            rope[min(warp + i * kAttnWarps, kHeadDim / 2 - 1)] = make_float4(cs[i].x, cs[i].y, rest[i].x, rest[i].y);
+    }
+    __syncthreads();
+    // the other stages' copies only now: before it they held up the loads above
+#pragma unroll
+    for (int s = 1; s < kStages - 1; ++s) {
+        if (next < tile_end) copy.issue(next, s, lane);
         cp_async_commit();
         next += kAttnWarps;
     }
-
-    // queries: one warp per head; the new row: the last warp of the last split
     if (warp < G) {
         float q[4];
-        norm_rope<float>(p.qkv + (size_t)(g * G + warp) * kHeadDim, p.q_norm, p.rope, p.eps, lane, q);
+        norm_rope(x, gain, rope, p.eps, lane, q);
         const float c = 1.4426950408889634f / sqrtf((float)kHeadDim);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) qs[warp][4 * lane + j] = q[j] * c;
-    }
-    if (has_new && warp == kAttnWarps - 1) {
-        // the new key in fp64 up to its rounding to bf16: its 4-bit codes are
-        // a step function of it, and must not depend on the order of a sum
-        double kd[4];
-        norm_rope<double>(p.qkv + (size_t)(p.n_q + g) * kHeadDim, p.k_norm, p.rope, p.eps, lane, kd);
-        const float* vs = p.qkv + (size_t)(p.n_q + p.n_kv + g) * kHeadDim + 4 * lane;
-        float kx[4], vx[4];
+        for (int j = 0; j < 4; ++j) q[j] *= c;
+        reinterpret_cast<float4*>(qs[warp])[lane] = make_float4(q[0], q[1], q[2], q[3]);
+        // the scores' operand.  Word w of a K row's 16-byte piece t holds channels
+        // 64 (w % 2) + 8 (2 t + w / 2) + 0..7; nibbles (0, 4) and (1, 5) are one
+        // product's rows, (2, 6) and (3, 7) the other's.  Codes come as an even
+        // nibble u and the whole byte u + 16 u': q u + q' u' = (q - q'/16) u +
+        // (q'/16) (u + 16 u')
+        const unsigned amax = __reduce_max_sync(
+            0xffffffffu, __float_as_uint(fmaxf(fmaxf(fabsf(q[0]), fabsf(q[1])), fmaxf(fabsf(q[2]), fabsf(q[3])))));
+        const int e = expo(__uint_as_float(amax));
+        const float f = to_2p15(e);
+        float sum = (q[0] + q[1]) + (q[2] + q[3]);
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if ((lane & 15) == 0) qhead[warp][lane >> 4] = sum;
+        if (lane == 0) qhead[warp][2] = pow2_field(min(10 + e, 254));  // 2^24 / f
+        const int unit = (lane & 15) >> 1, w = (lane >> 4) + 2 * (unit & 1);
+        __half* hi = reinterpret_cast<__half*>(&frag[0][w][0][4 * warp + (unit >> 1)]) + (lane & 1);
+        __half* lo = reinterpret_cast<__half*>(&frag[kParts - 1][w][0][4 * (kPack ? warp + 4 : warp) + (unit >> 1)]) + (lane & 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            kx[j] = round_bf16((float)kd[j]);
-            vx[j] = round_bf16(vs[j]);
+            const float v = (j & 1 ? 0.0625f * q[j] : q[j] - 0.0625f * q[j + 1]) * f;
+            const __half h = __float2half_rn(v);
+            const int at = (j >> 1) * (32 * 4) + (j & 1) * 2;
+            hi[at] = h;
+            lo[at] = __float2half_rn(v - __half2float(h));
         }
-        uint32_t kp, vp;
-        const uint32_t kc = quant_row(kx, &kp), vc = quant_row(vx, &vp);
-        const size_t at = base + p.pos;
-        store_row(kc, kp, p.k4 + at * kRowBytes, p.k_par + at * 2, lane);
-        store_row(vc, vp, p.v4 + at * kRowBytes, p.v_par + at * 2, lane);
+    }
+    // the new row: rounded to bf16, quantised, written to the cache, and kept as
+    // the cache holds it.  Only its own score waits for the queries, and nothing
+    // waits for it before the merge: its key takes longer than a query.
+    const auto store_new = [&](float v[4], uint8_t* codes, uint32_t* pars, int at_row, float4* keep) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float k = fmaf(bf16lo(kp), (float)((kc >> (4 * j)) & 15u), bf16hi(kp));
-            const float v = fmaf(bf16lo(vp), (float)((vc >> (4 * j)) & 15u), bf16hi(vp));
-            knew[4 * lane + j] = k;
-            vnew[4 * lane + j] = v;
-            if (p.kv_row) {
-                p.kv_row[(size_t)g * kHeadDim + 4 * lane + j] = k;
-                p.kv_row[(size_t)(p.n_kv + g) * kHeadDim + 4 * lane + j] = v;
+        for (int j = 0; j < 4; ++j) v[j] = round_bf16(v[j]);
+        uint32_t par;
+        const uint32_t code = quant_row(v, &par);
+        store_row(code, par, codes + (base + p.pos) * kRowBytes, pars + (base + p.pos) * 2, lane);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = fmaf(bf16lo(par), (float)((code >> (4 * j)) & 15u), bf16hi(par));
+        const float4 q = make_float4(v[0], v[1], v[2], v[3]);
+        if (keep) keep[lane] = q;
+        if (p.kv_row) reinterpret_cast<float4*>(p.kv_row)[(size_t)at_row * (kHeadDim / 4) + lane] = q;
+    };
+    constexpr int kThreads = kAttnWarps * 32;
+    if (new_k) {
+        asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
+        float k[4];
+        norm_rope_exact(x, gain, rope, p.eps, lane, k);
+        store_new(k, p.k4, p.k_par, g, nullptr);
+        asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
+        // the new position is a partial of its own: weight 1 at its score
+#pragma unroll
+        for (int j = 0; j < G; ++j) {
+            const float4 q = reinterpret_cast<const float4*>(qs[j])[lane];
+            const float s = warp_sum(fmaf(q.x, k[0], fmaf(q.y, k[1], fmaf(q.z, k[2], q.w * k[3]))));
+            if (lane == 0) {
+                wm[kAttnWarps][j] = s;
+                wl[kAttnWarps][j] = 1.f;
             }
         }
-    }
-    __syncthreads();
-    if (has_new && warp < G) {  // the new position: weight 1 at its own score
-        float s = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s = fmaf(qs[warp][4 * lane + j], knew[4 * lane + j], s);
-        s = warp_sum(s);
-        if (lane == 0) {
-            wm[kAttnWarps][warp] = s;
-            wl[kAttnWarps][warp] = 1.f;
+    } else {
+        if (new_v) {
+            float v[4] = {x.x, x.y, x.z, x.w};
+            store_new(v, p.v4, p.v_par, p.n_kv + g, reinterpret_cast<float4*>(vnew));
         }
+        asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+        if (has_new) asm volatile("bar.arrive 2, %0;" ::"n"(kThreads) : "memory");
     }
 
-    // query operand: word w of a K row's 16-byte piece t holds channels
-    // 64 (w % 2) + 8 (2 t + w / 2) + 0..7; nibbles (0, 4), (1, 5) are the first
-    // product's columns, (2, 6), (3, 7) the second's
-    uint32_t qa[4][2][4];
-    float fq = 0.f, qsum[2] = {0.f, 0.f};
+    // lane (r, t): positions r and r + 8 of a tile, query heads hd and hd + 1
+    // (packed: lanes t and t ^ 2 share them, one with the high parts' columns
+    // and one with the low parts')
+    const int hd = kPack ? 2 * (t & 1) : 2 * t;
+    uint2 qb[kParts][4][2];
     {
-        float amax = 0.f;
-        if (r < G) {
+        const bool used = !kPack || (r & 3) < G;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
 #pragma unroll
             for (int w = 0; w < 4; ++w)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float q = qs[r][64 * (w & 1) + 8 * (2 * t + (w >> 1)) + i];
-                    amax = fmaxf(amax, fabsf(q));
-                    qsum[w & 1] += q;
-                }
-        }
+                for (int i = 0; i < 2; ++i) qb[q][w][i] = used ? frag[q][w][i][lane] : make_uint2(0, 0);
+    }
+    float qsum[2][2], fq[2];
 #pragma unroll
-        for (int o = 1; o <= 2; o <<= 1) {
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            qsum[0] += __shfl_xor_sync(0xffffffffu, qsum[0], o);
-            qsum[1] += __shfl_xor_sync(0xffffffffu, qsum[1], o);
-        }
-        const int e = expo(amax);
-        const float f = to_2p15(e);
-        fq = pow2_field(min(10 + e, 254));  // 2^24 / f
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            float q[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                q[i] = r < G ? qs[r][64 * (w & 1) + 8 * (2 * t + (w >> 1)) + i] * f : 0.f;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                split_h2(q[2 * s], q[2 * s + 4], &qa[w][s][0], &qa[w][s][1]);
-                split_h2(q[2 * s + 1] * 0.0625f, q[2 * s + 5] * 0.0625f, &qa[w][s][2], &qa[w][s][3]);
-            }
-        }
+    for (int c = 0; c < 2; ++c) {
+        const bool used = hd + c < G;
+        qsum[0][c] = used ? qhead[hd + c][0] : 0.f;
+        qsum[1][c] = used ? qhead[hd + c][1] : 0.f;
+        fq[c] = used ? qhead[hd + c][2] : 0.f;
     }
 
-    float M = -INFINITY, l = 0.f, wmax[2] = {0.f, 0.f}, fv[2] = {to_2p15(14), to_2p15(14)}, omin[2] = {0.f, 0.f};
-    float o[2][8][4];
+    // M: the maximum the weights are relative to (it may lag the true one by
+    // up to 8, a factor 256, and is then moved for all lanes of a warp);
+    // fv[h]: the power of two that keeps |weight x V scale| of half h under
+    // 2^15; both per head.  l and omin are this lane's positions' shares.
+    float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, fv[2][2], omin[2][2] = {};
+    fv[0][0] = fv[0][1] = fv[1][0] = fv[1][1] = to_2p9(14);
+    float o[2][4][4];  // [half][16-channel block][row r: heads, row r + 8: heads]
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int c = 0; c < 4; ++c) o[h][i][c] = 0.f;
 
-    int stage = 0;
-    const int krow = 4 * (r >> 1) + (r & 1);
-    const int voff = (r >> 2) * 128 + (2 * t + ((r >> 1) & 1)) * 16 + (r & 1) * 8;
-    for (int tile = split * p.tiles_per_split + warp; tile < tile_end; tile += kAttnWarps) {
+    const uint8_t* kst = my_ring + r * kRowBytes + t * 16;
+    const uint8_t* vst = my_ring + kStageV + (r >> 2) * 128 + (2 * t + ((r >> 1) & 1)) * 16 + (r & 1) * 8;
+    const uint8_t* pst = my_ring + kStagePar + r * 8;
+    float sc[2][2];  // [position][head]
+    auto scores = [&](int so) {
+        const uint4 wa = *reinterpret_cast<const uint4*>(kst + so);
+        const uint4 wb = *reinterpret_cast<const uint4*>(kst + so + 8 * kRowBytes);
+        const uint2 par[2] = {*reinterpret_cast<const uint2*>(pst + so), *reinterpret_cast<const uint2*>(pst + so + 64)};
+        const uint32_t w[2][4] = {{wa.x, wa.y, wa.z, wa.w}, {wb.x, wb.y, wb.z, wb.w}};
+        float c[2][4];
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t u = bytes(w[0][i + h], s), v = bytes(w[1][i + h], s);
+                    const uint32_t a[4] = {u & 0x000f000fu, v & 0x000f000fu, u, v};
+                    if (i == 0 && s == 0)
+                        mma16816_first(c[h], a, qb[0][i + h][s]);
+                    else
+                        mma16816(c[h], a, qb[0][i + h][s]);
+                    if (!kPack) mma16816(c[h], a, qb[kParts - 1][i + h][s]);
+                }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float x = fmaf(c[1][2 * k + j], bf16lo(par[k].y), c[0][2 * k + j] * bf16lo(par[k].x));
+                if (kPack) x += __shfl_xor_sync(0xffffffffu, x, 2);
+                sc[k][j] = fmaf(x, fq[j], fmaf(bf16hi(par[k].x), qsum[0][j], bf16hi(par[k].y) * qsum[1][j]));
+            }
+    };
+    float wf[2][2][2];  // [half][position][head]
+    auto output = [&](int so) {
+        uint2 vw[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vw[i] = *reinterpret_cast<const uint2*>(vst + so + i * 256);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t hi[2], lo[2];
+            split_h2(wf[h][0][0], wf[h][0][1], &hi[0], &lo[0]);
+            split_h2(wf[h][1][0], wf[h][1][1], &hi[1], &lo[1]);
+            uint2 b[kParts];
+            if (kPack) {
+                b[0] = make_uint2(transpose8(t < 2 ? hi[0] : lo[0]), transpose8(t < 2 ? hi[1] : lo[1]));
+            } else {
+                b[0] = make_uint2(transpose8(hi[0]), transpose8(hi[1]));
+                b[kParts - 1] = make_uint2(transpose8(lo[0]), transpose8(lo[1]));
+            }
+            const uint32_t w0 = h ? vw[0].y : vw[0].x, w1 = h ? vw[1].y : vw[1].x;
+            const uint32_t w2 = h ? vw[2].y : vw[2].x, w3 = h ? vw[3].y : vw[3].x;
+            // block i: rows r are nibble 2 i of word r (channel 64 h + 8 r + 2 i),
+            // rows r + 8 that and 16 times nibble 2 i + 1
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t sel = i < 2 ? 0x5410u : 0x7632u;
+                const uint32_t x = bytes(__byte_perm(w0, w1, sel), i & 1), y = bytes(__byte_perm(w2, w3, sel), i & 1);
+                const uint32_t a[4] = {x & 0x000f000fu, x, y & 0x000f000fu, y};
+                mma16816(o[h][i], a, b[0]);
+                if (!kPack) mma16816(o[h][i], a, b[kParts - 1]);
+            }
+        }
+    };
+
+    int stage = 0, tile = split * p.tiles_per_split + warp;
+    if (tile < tile_end) {
         cp_async_wait<kStages - 2>();
+        __syncwarp();
+        scores(0);
+    }
+    for (; tile < tile_end; tile += kAttnWarps) {
         __syncwarp();
         {
             int fill = stage + kStages - 1;
             if (fill >= kStages) fill -= kStages;
-            if (next < tile_end) issue_tile(src, next, my_ring_s + fill * kStageBytes, lane);
+            if (next < tile_end) copy.issue(next, fill, lane);
             cp_async_commit();
             next += kAttnWarps;
         }
-        const uint8_t* st = my_ring + stage * kStageBytes;
+        const int so = stage * kStageBytes;
         if (++stage == kStages) stage = 0;
 
-        // ---- scores of positions 4t .. 4t + 3 for head r
-        float sc[4];
-        const uint4 kpa = *reinterpret_cast<const uint4*>(st + kStagePar + t * 32);
-        const uint4 kpb = *reinterpret_cast<const uint4*>(st + kStagePar + t * 32 + 16);
-        const uint32_t kpar[4][2] = {{kpa.x, kpa.y}, {kpa.z, kpa.w}, {kpb.x, kpb.y}, {kpb.z, kpb.w}};
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const uint4 w4 = *reinterpret_cast<const uint4*>(st + (krow + 2 * b) * kRowBytes + t * 16);
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-            float c[2][4] = {};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                mma16816(c[i & 1], qa[i][0], w[i] & 0x000f000fu, w[i] & 0x00f000f0u);
-                mma16816(c[i & 1], qa[i][1], (w[i] >> 8) & 0x000f000fu, (w[i] >> 8) & 0x00f000f0u);
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t* kp = kpar[2 * b + j];
-                const float x = fmaf(c[1][j] + c[1][2 + j], bf16lo(kp[1]), (c[0][j] + c[0][2 + j]) * bf16lo(kp[0]));
-                sc[2 * b + j] = fmaf(x, fq, fmaf(bf16hi(kp[0]), qsum[0], bf16hi(kp[1]) * qsum[1]));
-            }
-        }
         if (tile * kTilePos + kTilePos > p.pos) {
+            const int left = p.pos - tile * kTilePos - r;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (tile * kTilePos + 4 * t + k >= p.pos) sc[k] = -INFINITY;
+            for (int k = 0; k < 2; ++k)
+                if (8 * k >= left) sc[k][0] = sc[k][1] = -INFINITY;
+        }
+        float mx[2] = {fmaxf(sc[0][0], sc[1][0]), fmaxf(sc[0][1], sc[1][1])};
+        if (__any_sync(0xffffffffu, mx[0] > M[0] + 8.f || mx[1] > M[1] + 8.f)) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                for (int d = 4; d <= 16; d <<= 1) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], d));
+                if (mx[c] > M[c]) {
+                    const float corr = ex2(M[c] - mx[c]);
+                    M[c] = mx[c];
+                    l[c] *= corr;
+                    // weights so far shrink by corr: so does what they are kept under
+                    const int shrink = (int)(__float_as_uint(corr) >> 23) - 127;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int e_old = expo_of(fv[h][c]), e_new = max(e_old + shrink, 14);
+                        const float k = corr * pow2_field(min(127 + e_old - e_new, 254));
+                        fv[h][c] = to_2p9(e_new);
+                        omin[h][c] *= corr;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            o[h][i][c] *= k;
+                            o[h][i][2 + c] *= k;
+                        }
+                    }
+                }
+            }
         }
 
-        // ---- softmax weights, and the same times each position's V scale
-        float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float m_new = fmaxf(M, mx);
-        const uint4 vpa = *reinterpret_cast<const uint4*>(st + kStagePar + 128 + t * 32);
-        const uint4 vpb = *reinterpret_cast<const uint4*>(st + kStagePar + 128 + t * 32 + 16);
-        const uint32_t vpar[4][2] = {{vpa.x, vpa.y}, {vpa.z, vpa.w}, {vpb.x, vpb.y}, {vpb.z, vpb.w}};
-        float pw[4], ws[2][4], wx[2] = {0.f, 0.f}, lt = 0.f, ot[2] = {0.f, 0.f};
+        // ---- weights, and the same times each position's V scale
+        {
+            const uint2 par[2] = {*reinterpret_cast<const uint2*>(pst + so + 128),
+                                  *reinterpret_cast<const uint2*>(pst + so + 192)};
+            float wx = 0.f, vs[2][2][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            pw[k] = ex2(sc[k] - m_new);
-            lt += pw[k];
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                ws[h][k] = pw[k] * bf16lo(vpar[k][h]);
-                ot[h] = fmaf(pw[k], bf16hi(vpar[k][h]), ot[h]);
-                wx[h] = fmaxf(wx[h], fabsf(ws[h][k]));
+                for (int c = 0; c < 2; ++c) {
+                    const float pw = ex2(sc[k][c] - M[c]);
+                    l[c] += pw;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t u = h ? par[k].y : par[k].x;
+                        omin[h][c] = fmaf(pw, bf16hi(u), omin[h][c]);
+                        vs[h][k][c] = pw * bf16lo(u);
+                        wf[h][k][c] = vs[h][k][c] * fv[h][c];
+                        wx = fmaxf(wx, fabsf(wf[h][k][c]));
+                    }
+                }
+            if (__any_sync(0xffffffffu, wx >= 32768.f)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float m = fmaxf(fabsf(vs[h][0][c]), fabsf(vs[h][1][c]));
+#pragma unroll
+                        for (int d = 4; d <= 16; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                        const int e_old = expo_of(fv[h][c]), e_new = max(e_old, expo(m));
+                        const float k = pow2_field(max(127 + e_old - e_new, 0));
+                        fv[h][c] = to_2p9(e_new);
+                        wf[h][0][c] = vs[h][0][c] * fv[h][c];
+                        wf[h][1][c] = vs[h][1][c] * fv[h][c];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            o[h][i][c] *= k;
+                            o[h][i][2 + c] *= k;
+                        }
+                    }
             }
         }
-        wx[0] = fmaxf(wx[0], __shfl_xor_sync(0xffffffffu, wx[0], 1));
-        wx[1] = fmaxf(wx[1], __shfl_xor_sync(0xffffffffu, wx[1], 1));
-        wx[0] = fmaxf(wx[0], __shfl_xor_sync(0xffffffffu, wx[0], 2));
-        wx[1] = fmaxf(wx[1], __shfl_xor_sync(0xffffffffu, wx[1], 2));
-        const bool grew = m_new > M || expo(wx[0]) > expo(wmax[0]) || expo(wx[1]) > expo(wmax[1]);
-        if (__any_sync(0xffffffffu, grew)) {
-            const float corr = m_new > M ? ex2(M - m_new) : 1.f;
-            l *= corr;
-            M = m_new;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int e_old = expo(wmax[h]);
-                wmax[h] = fmaxf(wmax[h] * corr, wx[h]);
-                const int e_new = expo(wmax[h]);
-                fv[h] = to_2p15(e_new);
-                omin[h] *= corr;
-                // 2^(e_old - e_new), past the smallest normal power: nothing is left
-                const int d = 127 + e_old - e_new;
-                const float k = corr * pow2_field(max(0, min(d, 254)));
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) o[h][i][c] *= k;
-            }
-        }
-        l += lt;
-
-        // ---- output: V rows 4t .. 4t + 3, channels 64 h + 8 r + i
-        uint2 vw[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vw[i] = *reinterpret_cast<const uint2*>(st + kStageV + voff + i * 256);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            omin[h] += ot[h];
-            uint32_t a[4];
-            split_h2(ws[h][0] * fv[h], ws[h][1] * fv[h], &a[0], &a[1]);
-            split_h2(ws[h][2] * fv[h], ws[h][3] * fv[h], &a[2], &a[3]);
-            const uint32_t w0 = h ? vw[0].y : vw[0].x, w1 = h ? vw[1].y : vw[1].x;
-            const uint32_t w2 = h ? vw[2].y : vw[2].x, w3 = h ? vw[3].y : vw[3].x;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint32_t sel = half ? 0x7632u : 0x5410u;
-                const uint32_t x = __byte_perm(w0, w1, sel), y = __byte_perm(w2, w3, sel);
-                mma16816(o[h][4 * half + 0], a, x & 0x000f000fu, y & 0x000f000fu);
-                mma16816(o[h][4 * half + 1], a, x & 0x00f000f0u, y & 0x00f000f0u);
-                mma16816(o[h][4 * half + 2], a, (x >> 8) & 0x000f000fu, (y >> 8) & 0x000f000fu);
-                mma16816(o[h][4 * half + 3], a, (x >> 8) & 0x00f000f0u, (y >> 8) & 0x00f000f0u);
-            }
+        // the output product of this tile beside the scores of the next: two
+        // independent streams of tensor and integer work
+        if (tile + kAttnWarps < tile_end) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+            output(so);
+            scores(stage * kStageBytes);
+        } else {
+            output(so);
         }
     }
 
@@ -503,84 +691,160 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
     cp_async_wait<0>();
     __syncwarp();
 #pragma unroll
-    for (int d = 1; d <= 2; d <<= 1) {
-        l += __shfl_xor_sync(0xffffffffu, l, d);
-        omin[0] += __shfl_xor_sync(0xffffffffu, omin[0], d);
-        omin[1] += __shfl_xor_sync(0xffffffffu, omin[1], d);
-    }
-    if (r < G) {
-        if (t == 0) {
-            wm[warp][r] = M;
-            wl[warp][r] = l;
+    for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int d = 4; d <= 16; d <<= 1) {
+            l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
+            omin[0][c] += __shfl_xor_sync(0xffffffffu, omin[0][c], d);
+            omin[1][c] += __shfl_xor_sync(0xffffffffu, omin[1][c], d);
         }
-        float* po = reinterpret_cast<float*>(my_ring) + r * kHeadDim;
+        if (r == 0 && (!kPack || t < 2) && hd + c < G) {
+            wm[warp][hd + c] = M[c];
+            wl[warp][hd + c] = l[c];
+        }
+        float* po = reinterpret_cast<float*>(my_ring) + (hd + c) * kHeadDim + 8 * r;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float back = pow2_field(expo(wmax[h]));  // 2^e, and 2^24 2^-14 = 2^10 below
+            const float back = pow2_field(expo_of(fv[h][c]));  // 2^e, and 2^24 2^-8 = 2^16 below
+            float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float k = i & 1 ? 64.f : 1024.f;
-                po[64 * h + 8 * (2 * t) + i] = fmaf((o[h][i][0] + o[h][i][2]) * k, back, omin[h]);
-                po[64 * h + 8 * (2 * t + 1) + i] = fmaf((o[h][i][1] + o[h][i][3]) * k, back, omin[h]);
+                float x = i & 1 ? o[h][i >> 1][2 + c] - o[h][i >> 1][c] : o[h][i >> 1][c];
+                if (kPack) x += __shfl_xor_sync(0xffffffffu, x, 2);
+                v[i] = fmaf(x * (i & 1 ? 4096.f : 65536.f), back, omin[h][c]);
+            }
+            if ((!kPack || t < 2) && hd + c < G) {
+                reinterpret_cast<float4*>(po + 64 * h)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                reinterpret_cast<float4*>(po + 64 * h)[1] = make_float4(v[4], v[5], v[6], v[7]);
             }
         }
     }
     __syncthreads();
 
-    // ---- merge the warps and the new row.  A partial with sum 0 is empty; NaN
-    // sums pass through.
+    // ---- merge the warps and the new row, in order.  A partial with sum 0 is
+    // empty; NaN sums pass through.
     const int parts = has_new ? kAttnWarps + 1 : kAttnWarps;
     const size_t unit = (size_t)g * p.S + split;
-    for (int idx = threadIdx.x; idx < G * kHeadDim; idx += kAttnWarps * 32) {
-        const int j = idx / kHeadDim, d = idx % kHeadDim;
-        float mx = -INFINITY;
-        for (int w = 0; w < parts; ++w) mx = fmaxf(mx, wm[w][j]);
-        float L = 0.f, O = 0.f;
-        for (int w = 0; w < parts; ++w) {
-            if (wl[w][j] == 0.f) continue;
-            const float c = ex2(wm[w][j] - mx);
-            L += wl[w][j] * c;
-            O += (w < kAttnWarps ? reinterpret_cast<const float*>(ring + w * kRingBytes)[idx] : vnew[d]) * c;
+    if (warp < G) {
+        const bool in = lane < parts;
+        const float pm = in ? wm[lane][warp] : -INFINITY, pl = in ? wl[lane][warp] : 0.f;
+        const float mx = warp_max(pm);
+        const float c = pl == 0.f ? 0.f : ex2(pm - mx);
+        const float L = warp_sum(pl == 0.f ? 0.f : pl * c);
+        if (in) merge_c[lane][warp] = c;
+        if (lane == 0) {
+            merge_l[warp] = L;
+            if (p.S > 1) p.part_ml[unit * G + warp] = make_float2(mx, L);
+        }
+    }
+    __syncthreads();
+    constexpr int kVec = G * kHeadDim / 4;  // the group's outputs, four a thread
+    if (threadIdx.x < kVec) {
+        const int j = threadIdx.x / (kHeadDim / 4), d4 = threadIdx.x % (kHeadDim / 4);
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w <= kAttnWarps; ++w) {
+            if (w >= parts || wl[w][j] == 0.f) continue;  // an empty warp's ring holds no output
+            const float c = merge_c[w][j];
+            const float4 v = w < kAttnWarps ? reinterpret_cast<const float4*>(ring + w * kRingBytes)[threadIdx.x]
+                                            : reinterpret_cast<const float4*>(vnew)[d4];
+            O.x = fmaf(v.x, c, O.x);
+            O.y = fmaf(v.y, c, O.y);
+            O.z = fmaf(v.z, c, O.z);
+            O.w = fmaf(v.w, c, O.w);
         }
         if (p.S == 1) {
-            p.out[(size_t)g * G * kHeadDim + idx] = O / L;
+            const float L = merge_l[j];
+            reinterpret_cast<float4*>(p.out)[(size_t)g * kVec + threadIdx.x] = make_float4(O.x / L, O.y / L, O.z / L, O.w / L);
         } else {
-            p.part_o[unit * G * kHeadDim + idx] = O;
-            if (d == 0) p.part_ml[unit * G + j] = make_float2(mx, L);
+            reinterpret_cast<float4*>(p.part_o)[unit * kVec + threadIdx.x] = O;
         }
     }
     if (p.S == 1) return;
 
     // ---- the last split of this kv head to finish merges all splits, in order
-    __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) s_last = atomicAdd(&p.tickets[g], 1u) == (unsigned)(p.S - 1);
+    if (threadIdx.x == 0) {
+        // releases the block's partials (ordered before it by the barrier) and,
+        // for the last, acquires the others'
+        unsigned ticket;
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(ticket) : "l"(&p.tickets[g]) : "memory");
+        s_last = ticket == (unsigned)(p.S - 1);
+    }
     __syncthreads();
     if (!s_last) return;
-    __threadfence();
-    const float2* ml = p.part_ml + (size_t)g * p.S * G;
+    // thread (part, vector): every kTeams-th split, all its first loads in flight
+    // while the weights are found
+    constexpr int kTeams = kAttnWarps * 32 / kVec;
+    constexpr int kAhead = 8;
+    const int part = threadIdx.x / kVec, vec = threadIdx.x % kVec, head = vec / (kHeadDim / 4);
+    const float4* po = reinterpret_cast<const float4*>(p.part_o) + (size_t)g * p.S * kVec + vec;
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int s = part + i * kTeams;
+        ahead[i] = part < kTeams && s < p.S ? __ldcg(po + (size_t)s * kVec) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     if (warp < G) {
+        const float2* ml = p.part_ml + (size_t)g * p.S * G + warp;
+        constexpr int kMost = (kMaxSplitUnits + 31) / 32;
+        float2 v[kMost];
         float mx = -INFINITY;
-        for (int s = lane; s < p.S; s += 32) mx = fmaxf(mx, __ldcg(&ml[s * G + warp]).x);
+#pragma unroll
+        for (int i = 0; i < kMost; ++i) {
+            v[i] = lane + 32 * i < p.S ? __ldcg(ml + (size_t)(lane + 32 * i) * G) : make_float2(-INFINITY, 0.f);
+            mx = fmaxf(mx, v[i].x);
+        }
         mx = warp_max(mx);
         float L = 0.f;
-        for (int s = lane; s < p.S; s += 32) {
-            const float2 v = __ldcg(&ml[s * G + warp]);
-            const float c = ex2(v.x - mx);
-            merge_c[s][warp] = c;
-            L += v.y * c;
-        }
+#pragma unroll
+        for (int i = 0; i < kMost; ++i)
+            if (lane + 32 * i < p.S) {
+                const float c = ex2(v[i].x - mx);
+                merge_c[lane + 32 * i][warp] = c;
+                L = fmaf(v[i].y, c, L);
+            }
         L = warp_sum(L);
         if (lane == 0) merge_l[warp] = L;
     }
     __syncthreads();
-    const float* po = p.part_o + (size_t)g * p.S * G * kHeadDim;
-    for (int idx = threadIdx.x; idx < G * kHeadDim; idx += kAttnWarps * 32) {
-        const int j = idx / kHeadDim;
-        float O = 0.f;
-#pragma unroll 8
-        for (int s = 0; s < p.S; ++s) O = fmaf(__ldcg(po + (size_t)s * G * kHeadDim + idx), merge_c[s][j], O);
-        p.out[(size_t)g * G * kHeadDim + idx] = O / merge_l[j];
+    float4* parts_o = reinterpret_cast<float4*>(ring);  // [kTeams][kVec]
+    if (part < kTeams) {
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s0 = part; s0 < p.S; s0 += kAhead * kTeams) {
+            if (s0 != part) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    const int s = s0 + i * kTeams;
+                    if (s < p.S) ahead[i] = __ldcg(po + (size_t)s * kVec);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const int s = s0 + i * kTeams;
+                if (s >= p.S) break;
+                const float c = merge_c[s][head];
+                O.x = fmaf(ahead[i].x, c, O.x);
+                O.y = fmaf(ahead[i].y, c, O.y);
+                O.z = fmaf(ahead[i].z, c, O.z);
+                O.w = fmaf(ahead[i].w, c, O.w);
+            }
+        }
+        parts_o[threadIdx.x] = O;
+    }
+    __syncthreads();
+    if (threadIdx.x < kVec) {
+        float4 O = parts_o[threadIdx.x];
+#pragma unroll
+        for (int q = 1; q < kTeams; ++q) {
+            const float4 v = parts_o[q * kVec + threadIdx.x];
+            O.x += v.x;
+            O.y += v.y;
+            O.z += v.z;
+            O.w += v.w;
+        }
+        const float L = merge_l[head];
+        reinterpret_cast<float4*>(p.out)[(size_t)g * kVec + threadIdx.x] = make_float4(O.x / L, O.y / L, O.z / L, O.w / L);
     }
     if (threadIdx.x == 0) p.tickets[g] = 0u;
 }
@@ -610,7 +874,7 @@ int report_kv4(cudaError_t e, const char* what) {
 
 int max_splits(int n_kv) { return n_kv >= kMaxSplitUnits ? 1 : kMaxSplitUnits / n_kv; }
 
-// [tickets][maximum and sum: 2 words per split and query head][outputs: 128
+// [tickets][outputs: 128 words per split and query head][maximum and sum: 2
 // words per split and query head].  The tickets' place does not depend on the
 // heads, so a workspace may serve calls of different shapes in turn.
 size_t workspace_bytes_for(int n_q, int n_kv) {
@@ -712,17 +976,20 @@ extern "C" int tts_attention_decode_kv4(const float* qkv, const void* q_norm, co
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return TTS_ERR_CUDA;
-    // splits: at most one block per SM over all kv heads, at least a tile for
-    // every warp of a block, none empty
+    // splits: at most one block per SM over all kv heads, a tile for every warp
+    // of a block, none empty.  Up to two tiles a warp one block takes the whole
+    // head: 300 positions in 6.4 us against 7.0 in two blocks, whose merge costs
+    // more than the second round of tiles; 700 positions take 8.1 us in two
+    // blocks and 7.5 in three.
     const int tiles = (pos + kTilePos - 1) / kTilePos;
-    int S = (tiles + kAttnWarps - 1) / kAttnWarps;
+    int S = tiles <= 2 * kAttnWarps ? 1 : (tiles + kAttnWarps - 1) / kAttnWarps;
     S = std::max(1, std::min(S, std::min(max_splits(n_kv), sms / n_kv)));
     p.tiles_per_split = std::max(1, (tiles + S - 1) / S);
     p.S = std::max(1, (tiles + p.tiles_per_split - 1) / p.tiles_per_split);
     char* ws = static_cast<char*>(workspace);
     p.tickets = reinterpret_cast<unsigned*>(ws);
-    p.part_ml = reinterpret_cast<float2*>(ws + kTicketBytes);
-    p.part_o = reinterpret_cast<float*>(ws + kTicketBytes + sizeof(float2) * (size_t)n_q * max_splits(n_kv));
+    p.part_o = reinterpret_cast<float*>(ws + kTicketBytes);  // 16-byte vectors: before the 8-byte ones
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + (size_t)n_q * max_splits(n_kv) * kHeadDim);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (n_q / n_kv) {

@@ -388,7 +388,7 @@ int tts_quantize_fp8_weight(const void* W, int N, int K, void* W8, float* s, voi
  * tts_quantize_w4_weight makes them from W, DEVICE bf16 [N][K]: per group
  * s = bf16(max |w| / 7), u = 8 + clamp(rint(w / s), -8, 7) (IEEE fp32
  * divisions, rounding to nearest even; u = 8 where s is 0).  W finite.
- * K % 128 == 0; W and W4 16-byte aligned.  Enqueued on `stream` (NULL: the
+ * K % 128 == 0; W and W4 16-byte, s 4-byte aligned.  Enqueued on `stream` (NULL: the
  * default stream); does not synchronise.  TTS_ERR_ARG for bad sizes, NULL or
  * misaligned pointers. */
 int tts_quantize_w4_weight(const void* W, int N, int K, void* W4, void* s, void* stream);
@@ -403,7 +403,7 @@ int tts_quantize_w4_weight(const void* W, int N, int K, void* W4, void* s, void*
  *   fp32 [M][N] for epi 1 (may be y itself), NULL otherwise.
  * Activations stay fp32 (no rounding to 16 bits), sums are fp32, and every
  * result is deterministic.  1 <= M <= 8, K % 128 == 0, 128 <= K <= 12288, any
- * N from 1 to 2^24.  x, W4 and gamma 16-byte aligned; y overlaps no input
+ * N from 1 to 2^24.  x, W4 and gamma 16-byte, s 4-byte aligned; y overlaps no input
  * (but resid == y).  Enqueued on `stream` (NULL: the default stream); does
  * not synchronise; may be captured.  TTS_ERR_ARG otherwise. */
 int tts_gemv_w4(const float* x, const void* W4, const void* s, const float* resid, const void* gamma, float* y, int M,
@@ -441,8 +441,8 @@ int tts_dequantize_kv4(const void* k4, const void* v4, const void* k_par, const 
  * value (those of pos too) as the cache holds it.  qkv, q_norm, k_norm, out,
  * head counts as tts_attention_decode; max_pos up to 2^20, n_q up to 4096,
  * n_kv up to 1024.
- * Scores, softmax and sums are fp32, the new key is computed in fp64 up to
- * its rounding (its codes do not depend on the order of a sum), and every
+ * Scores, softmax and sums are fp32, the new key is computed to about 2^-44 up
+ * to its rounding (its codes do not depend on the order of a sum), and every
  * result is deterministic.  kv_row: DEVICE fp32 [2][n_kv][128], the key and
  * value of pos as the cache now holds them, or NULL.
  * workspace: DEVICE, at least tts_attention_kv4_workspace bytes, 16-byte

@@ -75,7 +75,7 @@ def quant_kv4(rows_bits):
     """bf16 bits [..., 128] -> (bytes [..., 64], parameter bits [..., 2, 2])."""
     x = bf16_val(rows_bits).astype(np.float32)
     x = x.reshape(x.shape[:-1] + (2, 64))
-    lo, hi = x.min(-1), x.max(-1)
+    lo, hi = x.min(-1) + np.float32(0), x.max(-1)  # a minimum of -0 is stored as 0
     s_bits = bf16_bits((hi - lo) / np.float32(15))
     s = bf16_val(s_bits).astype(np.float32)[..., None]
     with np.errstate(divide="ignore", invalid="ignore"):

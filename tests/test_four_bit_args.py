@@ -32,7 +32,7 @@ def test_quantize_w4_refusals(lib):
     good = dict(W=A[0], N=16, K=256, W4=A[1], s=A[2], stream=None)
     refuse(lib.tts_quantize_w4_weight, good,
            [dict(W=None), dict(W4=None), dict(s=None), dict(N=0), dict(N=-4), dict(K=0), dict(K=64), dict(K=200),
-            dict(W=A[0] + 8), dict(W4=A[1] + 4), dict(s=A[2] + 1)])
+            dict(W=A[0] + 8), dict(W4=A[1] + 4), dict(s=A[2] + 2)])
 
 
 def test_gemv_w4_refusals(lib):
@@ -42,7 +42,7 @@ def test_gemv_w4_refusals(lib):
            [dict(x=None), dict(W4=None), dict(s=None), dict(y=None), dict(M=0), dict(M=9), dict(N=0),
             dict(N=(1 << 24) + 1), dict(K=0), dict(K=192), dict(K=12416), dict(epi=3), dict(epi=-1),
             dict(epi=1), dict(resid=A[4]), dict(epi=2, resid=A[4]), dict(gamma=A[5], eps=-1.0),
-            dict(gamma=A[5], eps=float("nan")), dict(x=A[0] + 4), dict(W4=A[1] + 8), dict(s=A[2] + 1),
+            dict(gamma=A[5], eps=float("nan")), dict(x=A[0] + 4), dict(W4=A[1] + 8), dict(s=A[2] + 2),
             dict(y=A[3] + 2), dict(gamma=A[5] + 8), dict(epi=1, resid=A[4] + 2),
             # y over an input that other blocks still read
             dict(y=A[0]), dict(y=A[0] + 1020), dict(y=A[1] + 48 * 128 - 4), dict(y=A[2] + 48 * 4 - 4),
