@@ -79,14 +79,16 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const __nv_bfloat16* _
 // leave the tensor core once a group and are scaled and added in fp32:
 // acc += s (2^24-e part - 8 sum(a)).
 //
-// A block takes tiles of 16 rows (epi 2: a gate and an up tile), its warps one
-// slice of the groups each, the same for all its tiles, so a warp prepares its
-// slice of the activations once, for itself.  A lane copies exactly the 2 x 16
-// bytes a group that it uses (row r and r + 8, piece t), asynchronously into a
-// ring of its own: no barrier before a block's tiles are summed.
-constexpr int kMaxWarps = 16;
-constexpr int kRing = 4;      // items (tile, group) in flight a warp, 1 KB each
+// A block takes tiles of 16 rows (epi 2: a gate and an up tile), about one block
+// an SM; its warps take one slice of the groups each, the same for all its
+// tiles, so a warp prepares its slice of the activations once and for itself.
+// A lane copies exactly the 2 x 16 bytes of a group that it uses (rows r and
+// r + 8, piece t), asynchronously into a ring of its own: no barrier before all
+// of a block's tiles are done and the warps' sums are added.
+// (Four small blocks an SM were measured first: gate/up at one vector took
+// 11.7 us, most of it preparing the same activations four times.)
 constexpr int kMaxTiles = 8;  // tiles (epi 2: pairs) a block, at most
+constexpr int kStage = 1024 + 64;  // an item (tile, group): codes, then a word with each row's scale
 
 struct W4Launch {
     int warps, tiles, slice;  // tiles a block and groups a warp, at most
@@ -105,77 +107,34 @@ __device__ __forceinline__ uint32_t even_bytes(uint32_t w) { return w & 0x00ff00
 __device__ __forceinline__ uint32_t odd_bytes(uint32_t w) { return __byte_perm(w, 0u, 0x4341u); }
 
 // Shared memory of a warp: [ring][activations: slice x 4 words x 2 MV columns x
-// 4 pieces x 16 bytes][per group and vector: (2^24 over its power of two, 8 sum)]
-// [scales: tiles x 16 rows x the 4-byte words that cover a slice].
-__host__ __device__ inline int act_group_bytes(int mv) { return 4 * 2 * mv * 4 * 16; }
-__host__ __device__ inline int scale_words(int slice) { return slice / 2 + 1; }
-__host__ __device__ inline size_t warp_bytes(int mv, int slice, int tiles) {
-    const size_t b = (size_t)kRing * 1024 + (size_t)slice * act_group_bytes(mv) + (size_t)slice * mv * 8 +
-                     (size_t)tiles * 16 * scale_words(slice) * 4;
-    return (b + 15) & ~(size_t)15;
+// 4 pieces x 16 bytes][per group and vector: (2^24 over its power of two, 8 sum)].
+// Then the block's: [sums: tiles x parts x 16 rows x MV x warps][sums of squares].
+__host__ __device__ constexpr int act_group_bytes(int mv) { return 4 * 2 * mv * 4 * 16; }
+__host__ __device__ inline size_t warp_bytes(int mv, int ring, int slice) {
+    return ((size_t)ring * kStage + (size_t)slice * (act_group_bytes(mv) + mv * 8) + 15) & ~(size_t)15;
 }
+__host__ __device__ constexpr int max_warps(int mv) { return mv == 4 ? 16 : 24; }
 
-template <int MV>  // vectors of this block: 1, 2 or 4 columns pairs
-__global__ void __launch_bounds__(kMaxWarps * 32, MV == 1 ? 2 : 1) gemv_w4_kernel(const W4Params p, const W4Launch c) {
+template <int MV, int PARTS, int RING>  // vectors a block (1, 2, 4), tiles an output tile takes, items in flight a warp
+__global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4Params p, const W4Launch c) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = c.warps;
     const int r = lane >> 2, t = lane & 3;
-    const int groups = p.K / kW4Group, parts = p.epi == 2 ? 2 : 1;
-    const int g0 = (int)((long long)groups * warp / W), ng = (int)((long long)groups * (warp + 1) / W) - g0;
+    const int groups = p.K / kW4Group;
+    const int g0 = groups * warp / W, ng = groups * (warp + 1) / W - g0;  // at least 1: W <= groups
     const int m0 = blockIdx.y * MV, mv = min(MV, p.M - m0);
     const int ntiles = (p.N + 15) / 16;
     const int tile0 = blockIdx.x, step = gridDim.x;
     const int nt = (ntiles - tile0 + step - 1) / step;  // this block's tiles: tile0, tile0 + step, ...
-    const int rows_total = p.N * parts;
 
-    uint8_t* mine = smem + (size_t)warp * warp_bytes(MV, c.slice, c.tiles * parts);
-    uint8_t* act = mine + kRing * 1024;
+    uint8_t* mine = smem + (size_t)warp * warp_bytes(MV, RING, c.slice);
+    uint8_t* act = mine + RING * kStage;
     float2* act_par = reinterpret_cast<float2*>(act + c.slice * act_group_bytes(MV));
-    uint32_t* scl = reinterpret_cast<uint32_t*>(act_par + c.slice * MV);
-    float* sums = reinterpret_cast<float*>(smem + (size_t)W * warp_bytes(MV, c.slice, c.tiles * parts));
-    float* sq = sums + (size_t)c.tiles * parts * W * 16 * MV;  // [W][MV] sums of squares
+    float* sums = reinterpret_cast<float*>(smem + (size_t)W * warp_bytes(MV, RING, c.slice));
+    float* sq = sums + (size_t)c.tiles * PARTS * 16 * MV * W;  // [MV][W]
 
-    // row of the weights that row i of tile q = (tile, part) is; past the end, the
-    // last one (its result is not stored)
-    auto row_of = [&](int q, int i) {
-        const int tile = tile0 + (q / parts) * step;
-        return min(tile * 16 + i, p.N - 1) + (q % parts) * p.N;
-    };
-    const int items = nt * parts * ng;
-    const uint32_t ring = smem_u32(mine) + lane * 16;
-    int iq = 0, ig = 0;  // next item to copy
-    const uint8_t *pa = nullptr, *pb = nullptr;
-    auto issue = [&](int stage) {
-        if (ig == 0) {
-            pa = p.W4 + (size_t)row_of(iq, r) * (p.K / 2) + (size_t)g0 * 64 + t * 16;
-            pb = p.W4 + (size_t)row_of(iq, r + 8) * (p.K / 2) + (size_t)g0 * 64 + t * 16;
-        }
-        cp_async16_at(ring + stage * 1024, pa + ig * 64);
-        cp_async16_at(ring + stage * 1024 + 512, pb + ig * 64);
-        if (++ig == ng) { ig = 0; ++iq; }
-    };
-    int issued = 0;
-    // scales of all tiles first: 4-byte words that cover each row's slice
-    const int sw = scale_words(c.slice);
-    if (ng > 0) {
-        const long long total = (long long)rows_total * groups;  // scales in all
-        for (int i = lane; i < nt * parts * 16 * sw; i += 32) {
-            const int row = row_of(i / (16 * sw), (i / sw) & 15), wd = i % sw;
-            const long long at = ((long long)row * groups + g0) / 2 * 2 + 2 * wd;
-            if (at < (long long)row * groups + g0 + ng)
-                cp_async4_at(smem_u32(scl + i), p.s + at, at + 1 < total ? 4 : 2);
-        }
-    }
-    cp_async_commit_group();
-    for (; issued < kRing - 1; ++issued) {
-        if (issued < items) issue(issued);
-        cp_async_commit_group();
-    }
-
-    // ---- this warp's slice of the activations
-    float ss[MV];
-#pragma unroll
-    for (int m = 0; m < MV; ++m) ss[m] = 0.f;
+    // ---- activations of the slice's first group: before the copies, which would
+    // hold them up
     float4 xs[MV];
     uint2 gb = {};
     auto load_x = [&](int g) {
@@ -186,31 +145,87 @@ __global__ void __launch_bounds__(kMaxWarps * 32, MV == 1 ? 2 : 1) gemv_w4_kerne
         if (p.gamma) gb = *reinterpret_cast<const uint2*>(p.gamma + k);
     };
     load_x(0);
-    for (int g = 0; g < ng; ++g) {
-        float4 x4[MV];
-#pragma unroll
-        for (int m = 0; m < MV; ++m) x4[m] = xs[m];
-        float gm[4] = {1.f, 1.f, 1.f, 1.f};
-        if (p.gamma) {
-            gm[0] = bf16lo(gb.x);
-            gm[1] = bf16hi(gb.x);
-            gm[2] = bf16lo(gb.y);
-            gm[3] = bf16hi(gb.y);
+
+    // ---- copies, item by item: tile, part of it, group
+    const uint32_t ring = smem_u32(mine);
+    const long long total = (long long)p.N * PARTS * groups;  // scales in all
+    int iq = 0, ig = 0;                                       // next item to copy
+    const uint8_t *pa = nullptr, *pb = nullptr;
+    long long ps = 0;
+    // row i of the block's tile q; past the end the last row, whose result is not
+    // stored
+    auto row_of = [&](int q, int i) {
+        const int tile = tile0 + (q / PARTS) * step;
+        return min(tile * 16 + i, p.N - 1) + (q % PARTS) * p.N;
+    };
+    auto issue = [&](int stage) {
+        if (iq >= nt * PARTS) return;
+        if (ig == 0) {
+            pa = p.W4 + (size_t)row_of(iq, r) * (p.K / 2) + (size_t)g0 * 64 + t * 16;
+            pb = p.W4 + (size_t)row_of(iq, r + 8) * (p.K / 2) + (size_t)g0 * 64 + t * 16;
+            ps = (long long)row_of(iq, lane & 15) * groups + g0;
         }
-        if (g + 1 < ng) load_x(g + 1);
+        const uint32_t dst = ring + stage * kStage;
+        cp_async16_at(dst + lane * 16, pa + ig * 64);
+        cp_async16_at(dst + 512 + lane * 16, pb + ig * 64);
+        // the 4-byte word that holds the row's scale; the last one of all may be
+        // half a word
+        const long long at = (ps + ig) & ~1ll;
+        if (lane < 16) cp_async4_at(dst + 1024 + lane * 4, p.s + at, at + 1 < total ? 4 : 2);
+        if (++ig == ng) {
+            ig = 0;
+            ++iq;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < RING - 1; ++i) {
+        issue(i);
+        cp_async_commit_group();
+    }
+
+    // half-warp h of the block adds up output h, h + 2 W, ... at the end: what it
+    // adds the first of them to
+    const int half = threadIdx.x >> 4, h_lane = threadIdx.x & 15;
+    auto place = [&](int i, size_t* at) {  // output i: (tile, row, vector)
+        const int n = (tile0 + i / (16 * MV) * step) * 16 + (i / MV) % 16, m = i % MV;
+        *at = (size_t)(m0 + m) * p.N + n;
+        return i < nt * 16 * MV && n < p.N && m < mv;
+    };
+    float resid = 0.f;
+    if (p.resid && h_lane == 0) {
+        size_t at;
+        if (place(half, &at)) resid = p.resid[at];
+    }
+
+    // ---- this warp's slice of the activations
+    float ss[MV];
+#pragma unroll
+    for (int m = 0; m < MV; ++m) ss[m] = 0.f;
+    for (int g = 0; g < ng; ++g) {
+        float a[MV][4];
 #pragma unroll
         for (int m = 0; m < MV; ++m) {
-            float a[4] = {x4[m].x, x4[m].y, x4[m].z, x4[m].w};
+            a[m][0] = xs[m].x;
+            a[m][1] = xs[m].y;
+            a[m][2] = xs[m].z;
+            a[m][3] = xs[m].w;
             if (p.gamma) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    ss[m] = fmaf(a[j], a[j], ss[m]);
-                    a[j] *= gm[j];
-                }
+                for (int j = 0; j < 4; ++j) ss[m] = fmaf(a[m][j], a[m][j], ss[m]);
+                a[m][0] *= bf16lo(gb.x);
+                a[m][1] *= bf16hi(gb.x);
+                a[m][2] *= bf16lo(gb.y);
+                a[m][3] *= bf16hi(gb.y);
             }
-            const float sum = warp_sum((a[0] + a[1]) + (a[2] + a[3]));
+        }
+        if (g + 1 < ng) load_x(g + 1);
+        uint8_t* dst = act + (size_t)g * act_group_bytes(MV) + ((lane >> 1) & 3) * (2 * MV * 64) + (lane >> 3) * 16 + (lane & 1) * 8;
+#pragma unroll
+        for (int m = 0; m < MV; ++m) {
+            const float sum = warp_sum((a[m][0] + a[m][1]) + (a[m][2] + a[m][3]));
             const uint32_t amax = __reduce_max_sync(
-                0xffffffffu, __float_as_uint(fmaxf(fmaxf(fabsf(a[0]), fabsf(a[1])), fmaxf(fabsf(a[2]), fabsf(a[3])))));
+                0xffffffffu,
+                __float_as_uint(fmaxf(fmaxf(fabsf(a[m][0]), fabsf(a[m][1])), fmaxf(fabsf(a[m][2]), fabsf(a[m][3])))));
             // the group's power of two: largest to [2^14, 2^15)
             const int e = max((int)(amax >> 23), 14);
             const float f = __uint_as_float((uint32_t)(268 - e) << 23);
@@ -221,7 +236,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, MV == 1 ? 2 : 1) gemv_w4_kerne
             uint32_t hi[2], lo[2];  // (pair 0, pair 1), (pair 2, pair 3)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float v0 = (a[2 * j] - 0.0625f * a[2 * j + 1]) * f, v1 = 0.0625f * a[2 * j + 1] * f;
+                const float v0 = (a[m][2 * j] - 0.0625f * a[m][2 * j + 1]) * f, v1 = 0.0625f * a[m][2 * j + 1] * f;
                 const __half2 h = __floats2half2_rn(v0, v1);
                 const float2 hf = __half22float2(h);
                 const __half2 l = __floats2half2_rn(v0 - hf.x, v1 - hf.y);
@@ -233,40 +248,39 @@ __global__ void __launch_bounds__(kMaxWarps * 32, MV == 1 ? 2 : 1) gemv_w4_kerne
             const uint32_t gl = __shfl_xor_sync(0xffffffffu, odd ? lo[0] : lo[1], 1);
             const uint32_t eh = odd ? gh : hi[0], oh = odd ? hi[1] : gh;  // the even and the odd lane's halves
             const uint32_t el = odd ? gl : lo[0], ol = odd ? lo[1] : gl;
-            uint8_t* dst = act + (size_t)g * act_group_bytes(MV) + ((lane >> 1) & 3) * (2 * MV * 64) + 2 * m * 64 + (lane >> 3) * 16 +
-                           (odd ? 8 : 0);
-            *reinterpret_cast<uint2*>(dst) = make_uint2(__byte_perm(eh, oh, 0x5410), __byte_perm(eh, oh, 0x7632));
-            *reinterpret_cast<uint2*>(dst + 64) = make_uint2(__byte_perm(el, ol, 0x5410), __byte_perm(el, ol, 0x7632));
+            *reinterpret_cast<uint2*>(dst + 2 * m * 64) = make_uint2(__byte_perm(eh, oh, 0x5410), __byte_perm(eh, oh, 0x7632));
+            *reinterpret_cast<uint2*>(dst + 2 * m * 64 + 64) = make_uint2(__byte_perm(el, ol, 0x5410), __byte_perm(el, ol, 0x7632));
         }
     }
     if (p.gamma) {
 #pragma unroll
         for (int m = 0; m < MV; ++m) {
             ss[m] = warp_sum(ss[m]);
-            if (lane == 0) sq[warp * MV + m] = ss[m];
+            if (lane == 0) sq[m * W + warp] = ss[m];
         }
     }
     __syncwarp();
 
-    // ---- the products: items (tile, group) in order
-    int stage = 0, fill = kRing - 1;
+    // ---- the products
+    int stage = 0, fill = RING - 1;
     const bool column = r < 2 * MV;
     const uint8_t* my_act = act + r * 64 + t * 16;
-    for (int q = 0; q < nt * parts; ++q) {
+    for (int q = 0; q < nt * PARTS; ++q) {
         float acc[2] = {0.f, 0.f};
-        const long long ra = (long long)row_of(q, r) * groups + g0, rb = (long long)row_of(q, r + 8) * groups + g0;
-        const uint16_t* sa = reinterpret_cast<const uint16_t*>(scl + (q * 16 + r) * sw) + (ra & 1);
-        const uint16_t* sb = reinterpret_cast<const uint16_t*>(scl + (q * 16 + r + 8) * sw) + (rb & 1);
+        // which half of its word a row's first scale is
+        const int oa = (row_of(q, r) & groups & 1) ^ (g0 & 1), ob = (row_of(q, r + 8) & groups & 1) ^ (g0 & 1);
         for (int g = 0; g < ng; ++g) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+            asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
             __syncwarp();  // the scales come through other lanes' copies
-            if (issued < items) issue(fill);
-            ++issued;
+            issue(fill);
             cp_async_commit_group();
-            if (++fill == kRing) fill = 0;
-            const uint4 wa = *reinterpret_cast<const uint4*>(mine + stage * 1024 + lane * 16);
-            const uint4 wb = *reinterpret_cast<const uint4*>(mine + stage * 1024 + 512 + lane * 16);
-            if (++stage == kRing) stage = 0;
+            if (++fill == RING) fill = 0;
+            const uint8_t* st = mine + stage * kStage;
+            if (++stage == RING) stage = 0;
+            const uint4 wa = *reinterpret_cast<const uint4*>(st + lane * 16);
+            const uint4 wb = *reinterpret_cast<const uint4*>(st + 512 + lane * 16);
+            const uint32_t sa = *reinterpret_cast<const uint32_t*>(st + 1024 + r * 4);
+            const uint32_t sb = *reinterpret_cast<const uint32_t*>(st + 1024 + r * 4 + 32);
             const uint32_t ua[4] = {wa.x, wa.y, wa.z, wa.w}, ub[4] = {wb.x, wb.y, wb.z, wb.w};
             float d[2][4] = {};
 #pragma unroll
@@ -279,88 +293,95 @@ __global__ void __launch_bounds__(kMaxWarps * 32, MV == 1 ? 2 : 1) gemv_w4_kerne
             }
             const float2 ap = act_par[g * MV + (t < MV ? t : 0)];
             const float va = (d[0][0] + d[1][0]) + (d[0][1] + d[1][1]), vb = (d[0][2] + d[1][2]) + (d[0][3] + d[1][3]);
-            acc[0] = fmaf(bf16_bits_to_f32(sa[g]), fmaf(va, ap.x, -ap.y), acc[0]);
-            acc[1] = fmaf(bf16_bits_to_f32(sb[g]), fmaf(vb, ap.x, -ap.y), acc[1]);
+            acc[0] = fmaf((g ^ oa) & 1 ? bf16hi(sa) : bf16lo(sa), fmaf(va, ap.x, -ap.y), acc[0]);
+            acc[1] = fmaf((g ^ ob) & 1 ? bf16hi(sb) : bf16lo(sb), fmaf(vb, ap.x, -ap.y), acc[1]);
         }
         if (t < MV) {
-            float* s = sums + ((size_t)q * W + warp) * 16 * MV;
-            s[r * MV + t] = acc[0];
-            s[(r + 8) * MV + t] = acc[1];
+            float* s = sums + (size_t)(q * 16 * MV + t) * W + warp;
+            s[(size_t)r * MV * W] = acc[0];
+            s[(size_t)(r + 8) * MV * W] = acc[1];
         }
     }
-    cp_async_wait_all();
     __syncthreads();
 
-    // ---- the warps' sums, in order, and the epilogue
-    for (int i = threadIdx.x; i < nt * 16 * MV; i += W * 32) {
-        const int q = i / (16 * MV), row = (i / MV) & 15, m = i % MV;
-        const int n = (tile0 + q * step) * 16 + row;
-        if (n >= p.N || m >= mv) continue;
-        float v[2] = {0.f, 0.f};
-        for (int h = 0; h < parts; ++h)
-            for (int w = 0; w < W; ++w) v[h] += sums[((size_t)(q * parts + h) * W + w) * 16 * MV + row * MV + m];
-        if (p.gamma) {
-            float s2 = 0.f;
-            for (int w = 0; w < W; ++w) s2 += sq[w * MV + m];
-            const float rms = 1.f / sqrtf(s2 / (float)p.K + p.eps);
-            v[0] *= rms;
-            v[1] *= rms;
+    // ---- the warps' sums, an output a half-warp, and the epilogue
+    auto half_sum = [&](const float* v) {  // of W values, in a fixed order
+        float s = h_lane < W ? v[h_lane] : 0.f;
+        if (h_lane + 16 < W) s += v[h_lane + 16];
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        return s;
+    };
+    const int outs = nt * 16 * MV;
+    for (int i0 = 0; i0 < outs; i0 += 2 * W) {
+        const int i = i0 + half, at_i = min(i, outs - 1);
+        const int q = at_i / (16 * MV), rest = at_i % (16 * MV);
+        float v[PARTS], rms = 1.f;
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h) v[h] = half_sum(sums + (size_t)((q * PARTS + h) * 16 * MV + rest) * W);
+        if (p.gamma) rms = 1.f / sqrtf(half_sum(sq + (at_i % MV) * W) / (float)p.K + p.eps);
+        size_t at;
+        if (place(i, &at) && h_lane == 0) {
+            float y = v[0] * rms;
+            if (p.resid) y += i0 == 0 ? resid : p.resid[at];
+            if (PARTS == 2) y = y / (1.f + expf(-y)) * (v[PARTS - 1] * rms);
+            p.y[at] = y;
         }
-        const size_t at = (size_t)(m0 + m) * p.N + n;
-        float y = v[0];
-        if (p.epi == 1) y += p.resid[at];
-        if (p.epi == 2) y = y / (1.f + expf(-y)) * v[1];
-        p.y[at] = y;
     }
 }
 
 constexpr size_t kBlockSmem = 227 * 1024;
 
-// Tiles a block, warps a block and shared memory for p at MV vectors a block.
-W4Launch plan_gemv_w4(const W4Params& p, int mv, int ny, int sms) {
-    const int groups = p.K / kW4Group, parts = p.epi == 2 ? 2 : 1, ntiles = (p.N + 15) / 16;
+// Blocks, warps a block and tiles a block for p at MV vectors a block; ring is
+// set to the copies in flight a warp.
+W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, int ny, int sms, int* ring) {
+    const int groups = p.K / kW4Group, ntiles = (p.N + 15) / 16;
+    // a block an SM, which takes its tiles one after another
+    int grid = std::min(ntiles, std::max(1, sms / ny));
+    grid = std::max(grid, (ntiles + kMaxTiles - 1) / kMaxTiles);
+    const int tiles = (ntiles + grid - 1) / grid;
     W4Launch best{};
-    // blocks that an SM gets of this many tiles, and the warps of each that make
-    // about 24 an SM (enough copies in flight to cover the memory's latency)
-    const int per_sm = std::max(1, std::min(6, (ntiles * ny + sms / 2) / sms));
-    const int most = std::min(groups, std::max(4, std::min(kMaxWarps, 24 / per_sm)));
-    // of the warp counts down to half of that, the one that leaves the fewest idle
-    int warps = most;
-    for (int w = most; w >= (most + 1) / 2; --w)
-        if ((groups + w - 1) / w * w < (groups + warps - 1) / warps * warps) warps = w;
-    for (;; --warps) {
-        const int slice = (groups + warps - 1) / warps;
-        // a tile a block while the SMs hold all blocks at once, then as many tiles
-        // as it takes, for the activations are prepared once a block
-        for (int tiles = 1; tiles <= kMaxTiles; ++tiles) {
-            const size_t smem = warps * warp_bytes(mv, slice, tiles * parts) +
-                                4 * ((size_t)tiles * parts * warps * 16 * mv + (size_t)warps * mv);
-            if (smem > kBlockSmem) break;
-            best = W4Launch{warps, tiles, slice, (ntiles + tiles - 1) / tiles, smem};
-            // by shared memory and by registers (64, 92 and 110 a thread)
-            const int by_regs = (mv == 1 ? 32 : mv == 2 ? 20 : 16) / warps;
-            const int resident = std::max(1, std::min((int)(kBlockSmem / (smem + 1024)), by_regs));
-            if ((long long)best.grid * ny <= (long long)resident * sms) return best;
+    int best_cost = 1 << 30;
+    for (const int rg : {8, 3})
+        for (int w = std::min(groups, max_warps(mv)); w >= 1; --w) {
+            const int slice = (groups + w - 1) / w;
+            const size_t smem = w * warp_bytes(mv, rg, slice) + 4 * (size_t)w * mv * (tiles * parts * 16 + 1);
+            if (smem > kBlockSmem) continue;
+            // items of a tile that the fullest scheduler issues; under 12 warps
+            // they wait for one another more
+            const int cost = (w + 3) / 4 * slice * (w >= 12 ? 4 : 5);
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = W4Launch{w, tiles, slice, grid, smem};
+                *ring = rg;
+            }
         }
-        if (best.warps || warps == 1) return best;
+    return best;
+}
+
+template <int MV, int PARTS, int RING>
+cudaError_t launch_gemv_w4_as(const W4Params& p, const W4Launch& c, int ny, int dev, cudaStream_t s) {
+    static std::atomic<unsigned long long> ready{0};  // devices whose shared-memory limit is raised
+    const unsigned long long bit = 1ull << (dev & 63);
+    const auto kern = gemv_w4_kernel<MV, PARTS, RING>;
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBlockSmem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
     }
+    kern<<<dim3(c.grid, ny), c.warps * 32, c.smem, s>>>(p, c);
+    return cudaGetLastError();
 }
 
 template <int MV>
 cudaError_t launch_gemv_w4_mv(const W4Params& p, int dev, int sms, cudaStream_t s) {
-    static std::atomic<unsigned long long> ready{0};  // devices whose shared-memory limit is raised
-    const unsigned long long bit = 1ull << (dev & 63);
-    if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(gemv_w4_kernel<MV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBlockSmem);
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(bit, std::memory_order_relaxed);
-    }
     const int ny = (p.M + MV - 1) / MV;
-    const W4Launch c = plan_gemv_w4(p, MV, ny, sms);
+    int ring = 0;
+    const W4Launch c = plan_gemv_w4(p, MV, p.epi == 2 ? 2 : 1, ny, sms, &ring);
     if (!c.warps) return cudaErrorInvalidValue;
-    gemv_w4_kernel<MV><<<dim3(c.grid, ny), c.warps * 32, c.smem, s>>>(p, c);
-    return cudaGetLastError();
+    if (p.epi == 2)
+        return ring == 8 ? launch_gemv_w4_as<MV, 2, 8>(p, c, ny, dev, s) : launch_gemv_w4_as<MV, 2, 3>(p, c, ny, dev, s);
+    return ring == 8 ? launch_gemv_w4_as<MV, 1, 8>(p, c, ny, dev, s) : launch_gemv_w4_as<MV, 1, 3>(p, c, ny, dev, s);
 }
 
 cudaError_t launch_gemv_w4(const W4Params& p, int dev, int sms, cudaStream_t s) {
