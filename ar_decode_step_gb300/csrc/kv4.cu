@@ -90,46 +90,100 @@ __device__ __forceinline__ void store_row(uint32_t code, uint32_t par, uint8_t* 
     *reinterpret_cast<uint16_t*>(row + lane_byte(lane)) = (uint16_t)code;
     if ((lane & 15) == 0) par_row[lane >> 4] = par;
 }
-// Lane l's four values of a cached row.
-__device__ __forceinline__ void load_row(const uint8_t* row, const uint32_t* par_row, int lane, float v[4]) {
-    const uint32_t code = *reinterpret_cast<const uint16_t*>(row + lane_byte(lane));
-    const uint32_t par = par_row[lane >> 4];
+// ---- rows in and out ------------------------------------------------------------
+// Bound by memory (256 bytes of bf16 and 72 of codes and parameters a row).
+// A row is 16 lanes', 8 channels each: 16-byte accesses on the bf16 side, one
+// word of codes (a unit's share of a half) on the other.  A thread keeps
+// kRowsAhead rows in flight.
+constexpr int kRowThreads = 256;
+constexpr int kRowsAhead = 4;
+constexpr int kBlockRows = kRowThreads / 16 * kRowsAhead;
+
+struct RowParams {
+    const uint8_t *k4, *v4;
+    const uint32_t *k_par, *v_par;
+    const uint16_t *k, *v;
+    int p0, np, stride, max_pos;  // positions [p0, p0 + np); rows a head of the bf16 caches, of the 4-bit one
+};
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+
+__global__ void __launch_bounds__(kRowThreads) quantize_kv4_kernel(const RowParams p) {
+    const int head = blockIdx.y >> 1, lane = threadIdx.x & 15, h = lane >> 3, unit = lane & 7;
+    const bool is_v = blockIdx.y & 1;
+    const int i0 = blockIdx.x * kBlockRows + (threadIdx.x >> 4);
+    const uint16_t* src = (is_v ? p.v : p.k) + ((size_t)head * p.stride + p.p0) * kHeadDim + 8 * lane;
+    uint4 x[kRowsAhead];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = fmaf(bf16lo(par), (float)((code >> (4 * j)) & 15u), bf16hi(par));
+    for (int j = 0; j < kRowsAhead; ++j) {
+        const int i = min(i0 + 16 * j, p.np - 1);  // past the end the last row again, not stored
+        x[j] = *reinterpret_cast<const uint4*>(src + (size_t)i * kHeadDim);
+    }
+#pragma unroll
+    for (int j = 0; j < kRowsAhead; ++j) {
+        const int i = i0 + 16 * j;
+        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+        // minimum and maximum of the half, as one minimum of (x, -x); NaN stays NaN
+        __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(as_bf162(w[0]), as_bf162(w[1])), __hmin2_nan(as_bf162(w[2]), as_bf162(w[3])));
+        __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(as_bf162(w[0]), as_bf162(w[1])), __hmax2_nan(as_bf162(w[2]), as_bf162(w[3])));
+        __nv_bfloat162 both = __halves2bfloat162(__hmin_nan(__low2bfloat16(mn), __high2bfloat16(mn)),
+                                                 __hneg(__hmax_nan(__low2bfloat16(mx), __high2bfloat16(mx))));
+#pragma unroll
+        for (int d = 1; d <= 4; d <<= 1) both = __hmin2_nan(both, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(both), d)));
+        const float lo = __low2float(both) + 0.f, hi = -__high2float(both);  // + 0: a minimum of -0 is stored as 0
+        const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(hi - lo, 15.f));
+        const float s = __bfloat162float(sb);
+        uint32_t code = 0, par = 0x7fff7fffu;
+        if (isfinite(s)) {
+            par = (uint32_t)__bfloat16_as_ushort(sb) | (__float_as_uint(lo) & 0xffff0000u);
+            // as in quant_row; x >= lo, so a quotient is never negative, and adding
+            // 1.5 2^23 rounds it to the nearest even integer in the low bits
+            const float k = s < 0x1p-60f ? 0x1p100f : 1.f, ks = s * k, rs = __frcp_rn(ks);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float v = c & 1 ? bf16hi(w[c >> 1]) : bf16lo(w[c >> 1]);
+                const float q = fminf(div_rn_by((v - lo) * k, ks, rs), 15.f) + 12582912.f;
+                code |= (__float_as_uint(q) & 15u) << (4 * c);
+            }
+            if (!(s > 0.f)) code = 0;
+        }
+        if (i < p.np) {
+            const size_t at = (size_t)head * p.max_pos + p.p0 + i;
+            uint8_t* row = const_cast<uint8_t*>(is_v ? p.v4 : p.k4) + at * kRowBytes;
+            *reinterpret_cast<uint32_t*>(row + 8 * unit + 4 * h) = code;
+            if (unit == 0) const_cast<uint32_t*>(is_v ? p.v_par : p.k_par)[at * 2 + h] = par;
+        }
+    }
 }
 
-__global__ void __launch_bounds__(256) quantize_kv4_kernel(const uint16_t* k, const uint16_t* v, int n_kv, int p0,
-                                                           int np, int src_stride, uint8_t* k4, uint8_t* v4,
-                                                           uint32_t* k_par, uint32_t* v_par, int max_pos) {
-    const int lane = threadIdx.x & 31;
-    const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (i >= np) return;
-    const int head = blockIdx.y >> 1;
+__global__ void __launch_bounds__(kRowThreads) dequantize_kv4_kernel(const RowParams p) {
+    const int head = blockIdx.y >> 1, lane = threadIdx.x & 15, h = lane >> 3, unit = lane & 7;
     const bool is_v = blockIdx.y & 1;
-    const uint16_t* src = (is_v ? v : k) + ((size_t)head * src_stride + p0 + i) * kHeadDim + 4 * lane;
-    const uint2 w = *reinterpret_cast<const uint2*>(src);
-    const float x[4] = {bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y)};
-    uint32_t par;
-    const uint32_t code = quant_row(x, &par);
-    const size_t at = (size_t)head * max_pos + p0 + i;
-    store_row(code, par, (is_v ? v4 : k4) + at * kRowBytes, (is_v ? v_par : k_par) + at * 2, lane);
-}
-
-__global__ void __launch_bounds__(256) dequantize_kv4_kernel(const uint8_t* k4, const uint8_t* v4,
-                                                             const uint32_t* k_par, const uint32_t* v_par, int n_kv,
-                                                             int p0, int np, int max_pos, uint16_t* k, uint16_t* v,
-                                                             int dst_stride) {
-    const int lane = threadIdx.x & 31;
-    const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (i >= np) return;
-    const int head = blockIdx.y >> 1;
-    const bool is_v = blockIdx.y & 1;
-    const size_t at = (size_t)head * max_pos + p0 + i;
-    float x[4];
-    load_row((is_v ? v4 : k4) + at * kRowBytes, (is_v ? v_par : k_par) + at * 2, lane, x);
-    uint16_t* dst = (is_v ? v : k) + ((size_t)head * dst_stride + p0 + i) * kHeadDim + 4 * lane;
+    const int i0 = blockIdx.x * kBlockRows + (threadIdx.x >> 4);
+    const size_t first = (size_t)head * p.max_pos + p.p0;
+    const uint8_t* codes = (is_v ? p.v4 : p.k4) + first * kRowBytes + 8 * unit + 4 * h;
+    const uint32_t* pars = (is_v ? p.v_par : p.k_par) + first * 2 + h;
+    uint16_t* dst = const_cast<uint16_t*>(is_v ? p.v : p.k) + ((size_t)head * p.stride + p.p0) * kHeadDim + 8 * lane;
+    uint32_t code[kRowsAhead], par[kRowsAhead];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dst[j] = __bfloat16_as_ushort(__float2bfloat16_rn(x[j]));
+    for (int j = 0; j < kRowsAhead; ++j) {
+        const int i = min(i0 + 16 * j, p.np - 1);
+        code[j] = *reinterpret_cast<const uint32_t*>(codes + (size_t)i * kRowBytes);
+        par[j] = pars[(size_t)i * 2];
+    }
+#pragma unroll
+    for (int j = 0; j < kRowsAhead; ++j) {
+        const int i = i0 + 16 * j;
+        uint32_t w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint32_t b = code[j] >> (8 * c);
+            w[c] = as_u32(__floats2bfloat162_rn(fmaf(bf16lo(par[j]), (float)(b & 15u), bf16hi(par[j])),
+                                                fmaf(bf16lo(par[j]), (float)((b >> 4) & 15u), bf16hi(par[j]))));
+        }
+        if (i < p.np) *reinterpret_cast<uint4*>(dst + (size_t)i * kHeadDim) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 
 // q/k RMSNorm over the head then rotate-half RoPE: lane l has channels
@@ -907,11 +961,12 @@ extern "C" int tts_quantize_kv4(const void* k, const void* v, int n_kv, int p0, 
     using namespace tts;
     const int rc = rows_ok(k, v, k4, v4, k_par, v_par, n_kv, p0, p1, src_stride, max_pos);
     if (rc != TTS_OK || p0 == p1) return rc;
-    const dim3 grid((p1 - p0 + 7) / 8, 2 * n_kv);
-    quantize_kv4_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), n_kv, p0, p1 - p0, src_stride,
-        static_cast<uint8_t*>(k4), static_cast<uint8_t*>(v4), static_cast<uint32_t*>(k_par),
-        static_cast<uint32_t*>(v_par), max_pos);
+    const RowParams p{static_cast<const uint8_t*>(k4),      static_cast<const uint8_t*>(v4),
+                      static_cast<const uint32_t*>(k_par),  static_cast<const uint32_t*>(v_par),
+                      static_cast<const uint16_t*>(k),      static_cast<const uint16_t*>(v),
+                      p0, p1 - p0, src_stride, max_pos};
+    quantize_kv4_kernel<<<dim3((p.np + kBlockRows - 1) / kBlockRows, 2 * n_kv), kRowThreads, 0,
+                          static_cast<cudaStream_t>(stream)>>>(p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? TTS_OK : report_kv4(e, "tts_quantize_kv4");
 }
@@ -921,11 +976,12 @@ extern "C" int tts_dequantize_kv4(const void* k4, const void* v4, const void* k_
     using namespace tts;
     const int rc = rows_ok(k, v, k4, v4, k_par, v_par, n_kv, p0, p1, dst_stride, max_pos);
     if (rc != TTS_OK || p0 == p1) return rc;
-    const dim3 grid((p1 - p0 + 7) / 8, 2 * n_kv);
-    dequantize_kv4_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<const uint8_t*>(k4), static_cast<const uint8_t*>(v4), static_cast<const uint32_t*>(k_par),
-        static_cast<const uint32_t*>(v_par), n_kv, p0, p1 - p0, max_pos, static_cast<uint16_t*>(k),
-        static_cast<uint16_t*>(v), dst_stride);
+    const RowParams p{static_cast<const uint8_t*>(k4),      static_cast<const uint8_t*>(v4),
+                      static_cast<const uint32_t*>(k_par),  static_cast<const uint32_t*>(v_par),
+                      static_cast<const uint16_t*>(k),      static_cast<const uint16_t*>(v),
+                      p0, p1 - p0, dst_stride, max_pos};
+    dequantize_kv4_kernel<<<dim3((p.np + kBlockRows - 1) / kBlockRows, 2 * n_kv), kRowThreads, 0,
+                            static_cast<cudaStream_t>(stream)>>>(p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? TTS_OK : report_kv4(e, "tts_dequantize_kv4");
 }

@@ -1,7 +1,20 @@
 // Log probabilities of given codes, the entropy of the distribution and its
 // top alternatives, from the head's logits (sm_103a).
+//
+// Bound by reading the logits once (some 6 flops and one exponential a value).
+// A warp takes a run of up to 32 NV entries of a row into registers, lane l the
+// entries l, l + 32, ..., and finds there the maximum, the sums of e^z and
+// z e^z relative to it, and the `top` largest entries, without a second
+// reading.  A row of up to 1056 entries is one warp's (eight rows a block); a
+// longer one is shared by the warps of a block, or by a cluster of blocks when
+// there are few rows, whose results are joined through shared memory in a
+// fixed order, as a softmax over parts is.
+#include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdio>
+
+#include <cooperative_groups.h>
 
 #include "kernels.h"
 #include "tts_decode.h"
@@ -9,76 +22,299 @@
 namespace tts {
 namespace {
 
-// Sort key of entry i: larger logits first, equal ones by the lower index
-// (-0 equals +0; NaN below everything).
-__device__ __forceinline__ unsigned long long top_key(float z, int i) {
-    uint32_t b = __float_as_uint(z + 0.f);
-    b = (b & 0x80000000u) ? ~b : b | 0x80000000u;
-    if (isnan(z)) b = 0;
-    return (unsigned long long)b << 32 | (uint32_t)~i;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kRunNv = 33;                // 33 values a lane: 1026-entry codebooks in one run
+constexpr int kRun = 32 * kRunNv;
+constexpr int kShortWarps = 8;            // rows a block, short rows
+constexpr int kLongWarps = 16;            // warps a block, at most, long rows
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// fp32 bits (no NaN) as unsigned integers in the order of the values; -0 is 0.
+__device__ __forceinline__ uint32_t ranked(float z) {
+    const uint32_t b = __float_as_uint(z + 0.f);
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float from_ranked(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+constexpr uint32_t kRankedNone = 0x007fffffu;  // of -inf
+
+// What a part of a row comes to, its NaN entries left out: maximum m, l = sum
+// e^((z - m) / T), w = sum (z - m) e^((z - m) / T), and whether there was a NaN.
+// l = 0 where nothing is above -inf (and where m = +inf, which the caller sees).
+struct Part {
+    float m, l, w;
+    int nan;
+};
+// c = log2(e) / T.
+__device__ __forceinline__ Part join(const Part& a, const Part& b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    const float da = fmaxf(a.m - m, -3.0e38f), db = fmaxf(b.m - m, -3.0e38f);
+    const float fa = a.l > 0.f ? ex2(da * c) : 0.f, fb = b.l > 0.f ? ex2(db * c) : 0.f;
+    return Part{m, fa * a.l + fb * b.l, (fa > 0.f ? fa * (a.w + da * a.l) : 0.f) + (fb > 0.f ? fb * (b.w + db * b.l) : 0.f),
+                a.nan | b.nan};
+}
+// All lanes' parts joined, lane order fixed.
+__device__ __forceinline__ Part join_lanes(Part a, float c) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Part b{__shfl_xor_sync(kAll, a.m, o), __shfl_xor_sync(kAll, a.l, o), __shfl_xor_sync(kAll, a.w, o),
+                     __shfl_xor_sync(kAll, a.nan, o)};
+        a = join(a, b, c);
+    }
+    return a;
 }
 
-// One block per (row, codebook): maximum, sums, then one search per alternative.
-__global__ void __launch_bounds__(256) logprobs_kernel(const LogprobParams p) {
-    __shared__ float red[32];
-    __shared__ unsigned long long redk[8];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const size_t item = blockIdx.x;
-    const int V = p.V;
-    const float* z = p.logits + (item / p.n_cb) * p.ld + (item % p.n_cb) * V;
-    float m = -INFINITY, is_nan = 0.f;
-    for (int i = threadIdx.x; i < V; i += 256) {
-        m = fmaxf(m, z[i]);
-        if (isnan(z[i])) is_nan = 1.f;
+// One warp's run z[0 .. n), n <= 32 NV, entries numbered from `first`.  The list
+// (list_v, list_i): lane k has the k-th largest entry above -inf found so far
+// (-inf: none), equal ones by number; entries of the run join it, all numbered
+// above those it came with.
+template <int NV>
+__device__ __forceinline__ Part warp_run(const float* z, int n, int first, float c, int top, float& list_v, int& list_i) {
+    const int lane = threadIdx.x & 31;
+    float v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = lane + 32 * i < n ? __ldcs(z + lane + 32 * i) : -INFINITY;
+    // maxima of chunks of 8, so that a taken entry costs a search of one chunk
+    constexpr int kChunks = (NV + 7) / 8;
+    float cm[kChunks];
+    bool bad = false;
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+        cm[j] = -INFINITY;
+#pragma unroll
+        for (int i = 8 * j; i < 8 * j + 8 && i < NV; ++i) {
+            cm[j] = fmaxf(cm[j], v[i]);  // a NaN is passed over
+            bad |= v[i] != v[i];
+        }
     }
-    m = block_max(m, red);
-    const bool none = m == -INFINITY && block_max(is_nan, red) == 0.f;  // every entry is -inf
+    float m = cm[0];
+#pragma unroll
+    for (int j = 1; j < kChunks; ++j) m = fmaxf(m, cm[j]);
+    Part r;
+    r.nan = __any_sync(kAll, bad);
+    r.m = from_ranked(__reduce_max_sync(kAll, ranked(m)));
     float l = 0.f, w = 0.f;
-    for (int i = threadIdx.x; i < V; i += 256) {
-        const float d = z[i] - m, e = expf(d * p.inv_t);
-        l += e;
-        w += e > 0.f ? e * (d * p.inv_t) : 0.f;
+    if (r.m != -INFINITY && r.m != INFINITY) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const float d = fmaxf(v[i] - r.m, -3.0e38f);  // of -inf (and of NaN): e = 0
+            const float e = ex2(d * c);
+            l += e;
+            w = fmaf(e, d, w);
+        }
     }
-    l = block_sum(l, red);
-    w = block_sum(w, red);
-    const float logl = logf(l);
-    if (threadIdx.x == 0) {
+    r.l = warp_sum(l);
+    r.w = warp_sum(w);
+
+    if (top > 0) {
+        const float old_v = list_v;
+        const int old_i = list_i;
+        float have = old_v;  // the old list's entry while it is not taken: chunk 0, the lowest numbers
+        list_v = -INFINITY;
+        for (int k = 0; k < top; ++k) {
+            float best = have;
+#pragma unroll
+            for (int j = 0; j < kChunks; ++j) best = fmaxf(best, cm[j]);
+            const uint32_t key = ranked(best), most = __reduce_max_sync(kAll, key);
+            if (most <= kRankedNone) break;
+            const float b = from_ranked(most);
+            // of the lanes that hold it, the first chunk, then the lowest number in it
+            int chunk = kChunks;
+#pragma unroll
+            for (int j = kChunks - 1; j >= 0; --j)
+                if (cm[j] == b) chunk = j;
+            if (have == b) chunk = -1;
+            chunk = __reduce_min_sync(kAll, chunk);
+            int at = INT_MAX, q = -1;
+            if (chunk < 0) {
+                if (have == b) at = old_i;
+                const int win = __reduce_min_sync(kAll, at);
+                if (at == win) have = -INFINITY;
+                at = win;
+            } else {
+#pragma unroll
+                for (int j = 0; j < kChunks; ++j)
+                    if (chunk == j) {
+#pragma unroll
+                        for (int i = 8 * j + 7; i >= 8 * j; --i)
+                            if (i < NV && v[i] == b) q = i;
+                        if (q >= 0) at = first + 32 * q + lane;
+                        const int win = __reduce_min_sync(kAll, at);
+                        if (at != win) q = -1;
+                        at = win;
+                        cm[j] = -INFINITY;
+#pragma unroll
+                        for (int i = 8 * j; i < 8 * j + 8 && i < NV; ++i) {
+                            if (i == q) v[i] = -INFINITY;
+                            cm[j] = fmaxf(cm[j], v[i]);
+                        }
+                    }
+            }
+            if (lane == k) {
+                list_v = b;
+                list_i = at;
+            }
+        }
+    }
+    return r;
+}
+
+// The lists of n <= 32 parts, part q's entries at v[q * 32 .. q * 32 + 32), in order
+// of their numbers where values are equal; lane k gets the k-th of all.
+__device__ __forceinline__ void merge_lists(const float* v, const int* at, int n, int top, float& list_v, int& list_i) {
+    const int lane = threadIdx.x & 31;
+    int next = 0;
+    float head_v = lane < n ? v[lane * 32] : -INFINITY;
+    int head_i = lane < n ? at[lane * 32] : INT_MAX;
+    list_v = -INFINITY;
+    for (int k = 0; k < top; ++k) {
+        const uint32_t key = ranked(head_v), most = __reduce_max_sync(kAll, key);
+        if (most <= kRankedNone) break;
+        const int win = __reduce_min_sync(kAll, key == most ? head_i : INT_MAX);
+        if (lane == k) {
+            list_v = from_ranked(most);
+            list_i = win;
+        }
+        if (key == most && head_i == win) {
+            ++next;
+            head_v = next < 32 ? v[lane * 32 + next] : -INFINITY;
+            head_i = next < 32 ? at[lane * 32 + next] : INT_MAX;
+        }
+    }
+}
+
+// The results of row-and-codebook `item`, by one warp, from its joined part and
+// its list.  A list with fewer than `top` entries above -inf is filled up with
+// the -inf entries and then the NaN entries, by number: a search of the row.
+__device__ __forceinline__ void finish(const LogprobParams& p, size_t item, const float* z, const Part& r, float list_v,
+                                       int list_i) {
+    const int lane = threadIdx.x & 31;
+    const bool bad = r.nan || r.m == INFINITY, none = !bad && r.m == -INFINITY;
+    const float logl = logf(r.l);
+    auto logp = [&](float x) { return bad ? NAN : none ? -INFINITY : (x - r.m) * p.inv_t - logl; };
+    if (lane == 0) {
         if (p.logprob) {
             const int c = p.codes[item];
-            p.logprob[item] = c < 0 || c >= V ? NAN : none ? -INFINITY : (z[c] - m) * p.inv_t - logl;
+            p.logprob[item] = c < 0 || c >= p.V ? NAN : logp(z[c]);
         }
-        if (p.entropy) p.entropy[item] = none ? 0.f : logl - w / l;
+        if (p.entropy) p.entropy[item] = bad ? NAN : none ? 0.f : logl - r.w / r.l * p.inv_t;
     }
-    unsigned long long last = ~0ull;
-    for (int k = 0; k < p.top; ++k) {
-        unsigned long long best = 0;
-        for (int i = threadIdx.x; i < V; i += 256) {
-            const unsigned long long key = top_key(z[i], i);
-            if (key < last && key > best) best = key;
+    if (p.top == 0) return;
+    int got = __popc(__ballot_sync(kAll, lane < p.top && list_v != -INFINITY));
+    for (int pass = 0; pass < 2 && got < p.top; ++pass)
+        for (int i0 = 0; i0 < p.V && got < p.top; i0 += 32) {
+            const float x = i0 + lane < p.V ? z[i0 + lane] : 0.f;
+            unsigned found = __ballot_sync(kAll, pass ? x != x : x == -INFINITY);
+            for (; found && got < p.top; found &= found - 1, ++got)
+                if (lane == got) {
+                    list_v = -INFINITY;
+                    list_i = i0 + __ffs(found) - 1;
+                }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const unsigned long long other = __shfl_xor_sync(0xffffffffu, best, o);
-            best = other > best ? other : best;
-        }
-        __syncthreads();
-        if (lane == 0) redk[warp] = best;
-        __syncthreads();
-        for (int j = 0; j < 8; ++j) best = redk[j] > best ? redk[j] : best;
-        last = best;
-        if (threadIdx.x == 0) {
-            const int c = (int)~(uint32_t)best;
-            p.top_codes[item * p.top + k] = c;
-            p.top_logprob[item * p.top + k] = none ? -INFINITY : (z[c] - m) * p.inv_t - logl;
+    if (lane < p.top) {
+        p.top_codes[item * p.top + lane] = list_i;
+        p.top_logprob[item * p.top + lane] = logp(list_v);
+    }
+}
+
+__device__ __forceinline__ const float* row_of(const LogprobParams& p, size_t item) {
+    return p.logits + (item / p.n_cb) * p.ld + (item % p.n_cb) * (size_t)p.V;
+}
+
+template <int NV>
+__global__ void __launch_bounds__(kShortWarps * 32) logprobs_short_kernel(const LogprobParams p, int items) {
+    const int item = blockIdx.x * kShortWarps + (threadIdx.x >> 5);
+    if (item >= items) return;
+    const float* z = row_of(p, item);
+    float list_v = -INFINITY;
+    int list_i = 0;
+    const Part r = warp_run<NV>(z, p.V, 0, kLog2e * p.inv_t, p.top, list_v, list_i);
+    finish(p, item, z, r, list_v, list_i);
+}
+
+// A cluster of gridDim.y blocks a row: its warps take runs of the row in turn.
+__global__ void __launch_bounds__(kLongWarps * 32) logprobs_long_kernel(const LogprobParams p) {
+    __shared__ Part parts[kLongWarps];
+    __shared__ float lists_v[kLongWarps][32];
+    __shared__ int lists_i[kLongWarps][32];
+    // what the cluster's blocks hand to its first
+    __shared__ Part block_part[8];
+    __shared__ float block_v[8][32];
+    __shared__ int block_i[8][32];
+    namespace cg = cooperative_groups;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5, C = gridDim.y;
+    if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // all blocks run: awaited below
+    const size_t item = blockIdx.x;
+    const float* z = row_of(p, item);
+    const float c = kLog2e * p.inv_t;
+    Part r{-INFINITY, 0.f, 0.f, 0};
+    float list_v = -INFINITY;
+    int list_i = 0;
+    for (int first = ((int)blockIdx.y * W + warp) * kRun; first < p.V; first += C * W * kRun)
+        r = join(r, warp_run<kRunNv>(z + first, min(kRun, p.V - first), first, c, p.top, list_v, list_i), c);
+    if (lane == 0) parts[warp] = r;
+    lists_v[warp][lane] = list_v;
+    lists_i[warp][lane] = list_i;
+    if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    __syncthreads();
+    if (warp == 0) {
+        r = join_lanes(lane < W ? parts[lane] : Part{-INFINITY, 0.f, 0.f, 0}, c);
+        merge_lists(&lists_v[0][0], &lists_i[0][0], W, p.top, list_v, list_i);
+        if (C == 1) {
+            finish(p, item, z, r, list_v, list_i);
+        } else {
+            const auto cluster = cg::this_cluster();
+            const unsigned at = blockIdx.y;
+            if (lane == 0) *cluster.map_shared_rank(&block_part[at], 0) = r;
+            *cluster.map_shared_rank(&block_v[at][lane], 0) = list_v;
+            *cluster.map_shared_rank(&block_i[at][lane], 0) = list_i;
         }
     }
+    if (C == 1) return;
+    cg::this_cluster().sync();
+    if (blockIdx.y != 0 || warp != 0) return;
+    r = join_lanes(lane < C ? block_part[lane] : Part{-INFINITY, 0.f, 0.f, 0}, c);
+    merge_lists(&block_v[0][0], &block_i[0][0], C, p.top, list_v, list_i);
+    finish(p, item, z, r, list_v, list_i);
 }
 
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t s) {
-    logprobs_kernel<<<(unsigned)((long long)p.rows * p.n_cb), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    const int items = p.rows * p.n_cb;  // below 2^31: checked by the caller
+    if (p.V <= kRun) {
+        const unsigned grid = (items + kShortWarps - 1) / kShortWarps;
+        // 8 values a lane where that is enough: the 33 of a longer run would be
+        // mostly padding
+        if (p.V <= 256)
+            logprobs_short_kernel<8><<<grid, kShortWarps * 32, 0, s>>>(p, items);
+        else
+            logprobs_short_kernel<kRunNv><<<grid, kShortWarps * 32, 0, s>>>(p, items);
+        return cudaGetLastError();
+    }
+    const int runs = (p.V + kRun - 1) / kRun, W = std::min(kLongWarps, runs);
+    // one block a row, or so many that every warp has one run, while the rows do
+    // not fill the SMs by themselves
+    int C = 1;
+    while (C < 8 && C * W < runs && (long long)items * C < 152) C *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(items, C);
+    cfg.blockDim = dim3(W * 32);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1;
+    at[0].val.clusterDim.y = C;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = C > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, logprobs_long_kernel, p);
 }
 
 }  // namespace tts
@@ -89,8 +325,8 @@ extern "C" int tts_code_logprobs(const float* logits, long long ld, const int32_
     using namespace tts;
     if (rows < 0 || n_cb < 1 || n_cb > kMaxCodebooks || cb_vocab < 2 || cb_vocab > (1 << 20)) return TTS_ERR_ARG;
     if (!logits || ld < (long long)n_cb * cb_vocab || top < 0 || top > kMaxTop || top > cb_vocab) return TTS_ERR_ARG;
-    if ((long long)rows * n_cb > 0x7fffffffLL) return TTS_ERR_ARG;
-    if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.f / temperature)) return TTS_ERR_ARG;
+    if ((long long)rows * n_cb > 0x7fffffffLL - kShortWarps) return TTS_ERR_ARG;
+    if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(kLog2e / temperature)) return TTS_ERR_ARG;
     if ((logprob != nullptr) != (codes != nullptr)) return TTS_ERR_ARG;
     if ((top > 0) != (top_codes != nullptr) || (top > 0) != (top_logprob != nullptr)) return TTS_ERR_ARG;
     const uintptr_t all = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(codes) |
