@@ -132,21 +132,41 @@ __global__ void __launch_bounds__(kRowThreads) quantize_kv4_kernel(const RowPara
 #pragma unroll
         for (int d = 1; d <= 4; d <<= 1) both = __hmin2_nan(both, as_bf162(__shfl_xor_sync(0xffffffffu, as_u32(both), d)));
         const float lo = __low2float(both) + 0.f, hi = -__high2float(both);  // + 0: a minimum of -0 is stored as 0
-        const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(hi - lo, 15.f));
-        const float s = __bfloat162float(sb);
+        // s, its reciprocal and the quotients by one FMA correction each, IEEE results
+        // as quant_row's; very small ranges, where that does not hold, the slow way
+        const float range = hi - lo;
         uint32_t code = 0, par = 0x7fff7fffu;
-        if (isfinite(s)) {
-            par = (uint32_t)__bfloat16_as_ushort(sb) | (__float_as_uint(lo) & 0xffff0000u);
-            // as in quant_row; x >= lo, so a quotient is never negative, and adding
-            // 1.5 2^23 rounds it to the nearest even integer in the low bits
-            const float k = s < 0x1p-60f ? 0x1p100f : 1.f, ks = s * k, rs = __frcp_rn(ks);
+        if (range >= 0x1p-50f && isfinite(range)) {
+            constexpr float kFifteenth = 1.f / 15.f;
+            const __nv_bfloat16 sb = __float2bfloat16_rn(div_rn_by(range, 15.f, kFifteenth));
+            const float s = __bfloat162float(sb), rs = __frcp_rn(s);
+            if (isfinite(s)) par = (uint32_t)__bfloat16_as_ushort(sb) | (__float_as_uint(lo) & 0xffff0000u);
+            const f32x2 ml = pack2(-lo, -lo), ms = pack2(-s, -s), rr = pack2(rs, rs);
+            // 1.5 2^23 added and taken away rounds to the nearest even integer; s has 8
+            // bits of (max - min) / 15, so no quotient rounds above 15
+            const f32x2 magic = pack2(12582912.f, 12582912.f), back = pack2(-12582912.f, -12582912.f);
+            float u[8];
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const float v = c & 1 ? bf16hi(w[c >> 1]) : bf16lo(w[c >> 1]);
-                const float q = fminf(div_rn_by((v - lo) * k, ks, rs), 15.f) + 12582912.f;
-                code |= (__float_as_uint(q) & 15u) << (4 * c);
+            for (int c = 0; c < 4; ++c) {
+                const f32x2 d = add2(pack2(bf16lo(w[c]), bf16hi(w[c])), ml), q0 = mul2(d, rr);
+                const f32x2 q = fma2(fma2(q0, ms, d), rr, q0);
+                const float2 n = unpack2(add2(add2(q, magic), back));
+                u[2 * c] = n.x;
+                u[2 * c + 1] = n.y;
             }
-            if (!(s > 0.f)) code = 0;
+            // four codes as one exact integer below 2^16, in the low bits of 2^23 + it
+            const float c0 = fmaf(4096.f, u[3], fmaf(256.f, u[2], fmaf(16.f, u[1], u[0]))) + 8388608.f;
+            const float c1 = fmaf(4096.f, u[7], fmaf(256.f, u[6], fmaf(16.f, u[5], u[4]))) + 8388608.f;
+            code = isfinite(s) ? __byte_perm(__float_as_uint(c0), __float_as_uint(c1), 0x5410) : 0u;
+        } else if (isfinite(range)) {
+            const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(range, 15.f));
+            const float s = __bfloat162float(sb);
+            par = (uint32_t)__bfloat16_as_ushort(sb) | (__float_as_uint(lo) & 0xffff0000u);
+            const float ks = s * 0x1p100f, rs = __frcp_rn(ks);
+            for (int c = 0; c < 8 && s > 0.f; ++c) {
+                const float v = __uint_as_float(c & 1 ? w[c >> 1] & 0xffff0000u : w[c >> 1] << 16);
+                code |= (uint32_t)fminf(rintf(div_rn_by((v - lo) * 0x1p100f, ks, rs)), 15.f) << (4 * c);
+            }
         }
         if (i < p.np) {
             const size_t at = (size_t)head * p.max_pos + p.p0 + i;
@@ -175,13 +195,21 @@ __global__ void __launch_bounds__(kRowThreads) dequantize_kv4_kernel(const RowPa
 #pragma unroll
     for (int j = 0; j < kRowsAhead; ++j) {
         const int i = i0 + 16 * j;
-        uint32_t w[4];
+        // a nibble in a 16-bit half is the fp16 subnormal u 2^-24: scale and minimum in
+        // one FMA (s 2^24 is exact but for the largest scales, which go the long way)
+        const float s = bf16lo(par[j]), m = bf16hi(par[j]);
+        const bool large = !(fabsf(s) < 0x1p100f);
+        const f32x2 ss = large ? pack2(s, s) : pack2(s * 16777216.f, s * 16777216.f), mm = pack2(m, m);
+        float2 f[4];  // channels (0, 4), (1, 5), (2, 6), (3, 7)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const uint32_t b = code[j] >> (8 * c);
-            w[c] = as_u32(__floats2bfloat162_rn(fmaf(bf16lo(par[j]), (float)(b & 15u), bf16hi(par[j])),
-                                                fmaf(bf16lo(par[j]), (float)((b >> 4) & 15u), bf16hi(par[j]))));
+            const uint32_t u = (code[j] >> (4 * c)) & 0x000f000fu;
+            float2 x = __half22float2(*reinterpret_cast<const __half2*>(&u));
+            if (large) x = make_float2(x.x * 16777216.f, x.y * 16777216.f);
+            f[c] = unpack2(fma2(pack2(x.x, x.y), ss, mm));
         }
+        const uint32_t w[4] = {as_u32(__floats2bfloat162_rn(f[0].x, f[1].x)), as_u32(__floats2bfloat162_rn(f[2].x, f[3].x)),
+                               as_u32(__floats2bfloat162_rn(f[0].y, f[1].y)), as_u32(__floats2bfloat162_rn(f[2].y, f[3].y))};
         if (i < p.np) *reinterpret_cast<uint4*>(dst + (size_t)i * kHeadDim) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }

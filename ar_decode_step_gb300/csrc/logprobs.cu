@@ -70,108 +70,194 @@ __device__ __forceinline__ Part join_lanes(Part a, float c) {
     return a;
 }
 
+// The `top` (at most 32) largest of up to 32 candidates above -inf, one a lane
+// (cand_v = -inf: none), largest first, equal ones by number: lane k gets the k-th.
+__device__ __forceinline__ void sort_candidates(float cand_v, int cand_i, int top, float& list_v, int& list_i) {
+    const int lane = threadIdx.x & 31;
+    uint32_t key = ranked(cand_v);
+    list_v = -INFINITY;
+    for (int k = 0; k < top; ++k) {
+        const uint32_t most = __reduce_max_sync(kAll, key);
+        if (most <= kRankedNone) break;
+        const int win = __reduce_min_sync(kAll, key == most ? cand_i : INT_MAX);
+        if (key == most && cand_i == win) key = 0;
+        if (lane == k) {
+            list_v = from_ranked(most);
+            list_i = win;
+        }
+    }
+}
+
+struct Candidates {
+    float v[32];
+    int i[32];
+};
+
 // One warp's run z[0 .. n), n <= 32 NV, entries numbered from `first`.  The list
 // (list_v, list_i): lane k has the k-th largest entry above -inf found so far
 // (-inf: none), equal ones by number; entries of the run join it, all numbered
 // above those it came with.
+//
+// Alternatives: the `top`-th largest of the 32 lanes' maxima is a bound that the
+// `top` largest entries reach, and few others do; those that do are gathered, one
+// a lane, and sorted.  Where more than 32 do (many alternatives, ties) or fewer
+// than `top` lanes have an entry at all, they are taken out one by one instead.
+// (One by one throughout took 41 us on 4096 frames x 8 x 1026 with 5 alternatives,
+// twice as many instructions.)
 template <int NV>
-__device__ __forceinline__ Part warp_run(const float* z, int n, int first, float c, int top, float& list_v, int& list_i) {
+__device__ __forceinline__ Part warp_run(const float* z, int n, int first, float c, int top, Candidates& cand,
+                                         float& list_v, int& list_i) {
     const int lane = threadIdx.x & 31;
-    float v[NV];
+    float v[NV + (NV & 1)];
+    if (n >= 32 * (NV - 1)) {  // all but the last load unguarded
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = lane + 32 * i < n ? __ldcs(z + lane + 32 * i) : -INFINITY;
-    // maxima of chunks of 8, so that a taken entry costs a search of one chunk
+        for (int i = 0; i < NV - 1; ++i) v[i] = __ldcs(z + lane + 32 * i);
+        v[NV - 1] = lane + 32 * (NV - 1) < n ? __ldcs(z + lane + 32 * (NV - 1)) : -INFINITY;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[i] = lane + 32 * i < n ? __ldcs(z + lane + 32 * i) : -INFINITY;
+    }
+    if (NV & 1) v[NV] = -INFINITY;
+    // maxima of chunks of 8 (a NaN is passed over)
     constexpr int kChunks = (NV + 7) / 8;
     float cm[kChunks];
-    bool bad = false;
 #pragma unroll
     for (int j = 0; j < kChunks; ++j) {
-        cm[j] = -INFINITY;
+        cm[j] = v[8 * j];
 #pragma unroll
-        for (int i = 8 * j; i < 8 * j + 8 && i < NV; ++i) {
-            cm[j] = fmaxf(cm[j], v[i]);  // a NaN is passed over
-            bad |= v[i] != v[i];
-        }
+        for (int i = 8 * j + 1; i < 8 * j + 8 && i < NV; ++i) cm[j] = fmaxf(cm[j], v[i]);
+        cm[j] = fmaxf(cm[j], -INFINITY);
     }
     float m = cm[0];
 #pragma unroll
     for (int j = 1; j < kChunks; ++j) m = fmaxf(m, cm[j]);
     Part r;
-    r.nan = __any_sync(kAll, bad);
     r.m = from_ranked(__reduce_max_sync(kAll, ranked(m)));
-    float l = 0.f, w = 0.f;
+    r.l = r.w = 0.f;
     if (r.m != -INFINITY && r.m != INFINITY) {
+        const f32x2 minus = pack2(-r.m, -r.m), cc = pack2(c, c);
+        f32x2 l = pack2(0.f, 0.f), w = l;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const float d = fmaxf(v[i] - r.m, -3.0e38f);  // of -inf (and of NaN): e = 0
-            const float e = ex2(d * c);
-            l += e;
-            w = fmaf(e, d, w);
+        for (int i = 0; i < NV; i += 2) {
+            const f32x2 d = add2(pack2(v[i], v[i + 1]), minus);
+            const float2 a = unpack2(mul2(d, cc)), b = unpack2(d);
+            const f32x2 e = pack2(ex2(a.x), ex2(a.y));
+            l = add2(l, e);                                                    // NaN where an entry is NaN
+            w = fma2(e, pack2(fmaxf(b.x, -3.0e38f), fmaxf(b.y, -3.0e38f)), w);  // an entry of -inf adds 0
+        }
+        const float2 ls = unpack2(l), wsum = unpack2(w);
+        r.l = warp_sum(ls.x + ls.y);
+        r.w = warp_sum(wsum.x + wsum.y);
+        r.nan = r.l != r.l;
+        if (r.nan) r.l = r.w = 0.f;
+    } else {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) bad |= v[i] != v[i];
+        r.nan = __any_sync(kAll, bad);
+    }
+    if (top == 0) return r;
+
+    const float old_v = list_v;
+    const int old_i = list_i;
+    // the bound
+    float bound = -INFINITY;
+    {
+        uint32_t key = ranked(fmaxf(m, old_v));
+        for (int k = 0; k < top; ++k) {
+            const uint32_t most = __reduce_max_sync(kAll, key);
+            bound = most > kRankedNone ? from_ranked(most) : -INFINITY;
+            if (most <= kRankedNone) break;
+            if (lane == __ffs(__ballot_sync(kAll, key == most)) - 1) key = 0;
         }
     }
-    r.l = warp_sum(l);
-    r.w = warp_sum(w);
+    int count = 33;
+    if (bound != -INFINITY) {
+        count = 0;
+        auto gather = [&](float x, int at) {
+            const unsigned in = __ballot_sync(kAll, x >= bound);
+            if (in) {
+                const int place = count + __popc(in & ((1u << lane) - 1));
+                if (x >= bound && place < 32) {
+                    cand.v[place] = x;
+                    cand.i[place] = at;
+                }
+                count += __popc(in);
+            }
+        };
+        gather(old_v, old_i);
+#pragma unroll
+        for (int j = 0; j < kChunks; ++j)
+            if (__any_sync(kAll, cm[j] >= bound)) {
+#pragma unroll
+                for (int i = 8 * j; i < 8 * j + 8 && i < NV; ++i) gather(v[i], first + 32 * i + lane);
+            }
+    }
+    if (count <= 32) {
+        __syncwarp();
+        const float cv = lane < count ? cand.v[lane] : -INFINITY;
+        const int ci = lane < count ? cand.i[lane] : INT_MAX;
+        __syncwarp();
+        sort_candidates(cv, ci, top, list_v, list_i);
+        return r;
+    }
 
-    if (top > 0) {
-        const float old_v = list_v;
-        const int old_i = list_i;
-        float have = old_v;  // the old list's entry while it is not taken: chunk 0, the lowest numbers
-        list_v = -INFINITY;
-        for (int k = 0; k < top; ++k) {
-            float best = have;
+    float have = old_v;  // the old list's entry while it is not taken: chunk -1, the lowest numbers
+    list_v = -INFINITY;
+    for (int k = 0; k < top; ++k) {
+        float best = have;
 #pragma unroll
-            for (int j = 0; j < kChunks; ++j) best = fmaxf(best, cm[j]);
-            const uint32_t key = ranked(best), most = __reduce_max_sync(kAll, key);
-            if (most <= kRankedNone) break;
-            const float b = from_ranked(most);
-            // of the lanes that hold it, the first chunk, then the lowest number in it
-            int chunk = kChunks;
+        for (int j = 0; j < kChunks; ++j) best = fmaxf(best, cm[j]);
+        const uint32_t most = __reduce_max_sync(kAll, ranked(best));
+        if (most <= kRankedNone) break;
+        const float b = from_ranked(most);
+        // of the lanes that hold it, the first chunk, then the lowest number in it
+        int chunk = kChunks;
 #pragma unroll
-            for (int j = kChunks - 1; j >= 0; --j)
-                if (cm[j] == b) chunk = j;
-            if (have == b) chunk = -1;
-            chunk = __reduce_min_sync(kAll, chunk);
-            int at = INT_MAX, q = -1;
-            if (chunk < 0) {
-                if (have == b) at = old_i;
-                const int win = __reduce_min_sync(kAll, at);
-                if (at == win) have = -INFINITY;
-                at = win;
-            } else {
+        for (int j = kChunks - 1; j >= 0; --j)
+            if (cm[j] == b) chunk = j;
+        if (have == b) chunk = -1;
+        chunk = __reduce_min_sync(kAll, chunk);
+        int at = INT_MAX;
+        if (chunk < 0) {
+            if (have == b) at = old_i;
+            const int win = __reduce_min_sync(kAll, at);
+            if (at == win) have = -INFINITY;
+            at = win;
+        } else {
 #pragma unroll
-                for (int j = 0; j < kChunks; ++j)
-                    if (chunk == j) {
+            for (int j = 0; j < kChunks; ++j)
+                if (chunk == j) {
+                    int q = -1;
 #pragma unroll
-                        for (int i = 8 * j + 7; i >= 8 * j; --i)
-                            if (i < NV && v[i] == b) q = i;
-                        if (q >= 0) at = first + 32 * q + lane;
-                        const int win = __reduce_min_sync(kAll, at);
-                        if (at != win) q = -1;
-                        at = win;
-                        cm[j] = -INFINITY;
+                    for (int i = 8 * j + 7; i >= 8 * j; --i)
+                        if (i < NV && v[i] == b) q = i;
+                    if (q >= 0) at = first + 32 * q + lane;
+                    const int win = __reduce_min_sync(kAll, at);
+                    if (at != win) q = -1;
+                    at = win;
+                    cm[j] = -INFINITY;
 #pragma unroll
-                        for (int i = 8 * j; i < 8 * j + 8 && i < NV; ++i) {
-                            if (i == q) v[i] = -INFINITY;
-                            cm[j] = fmaxf(cm[j], v[i]);
-                        }
+                    for (int i = 8 * j; i < 8 * j + 8 && i < NV; ++i) {
+                        if (i == q) v[i] = -INFINITY;
+                        cm[j] = fmaxf(cm[j], v[i]);
                     }
-            }
-            if (lane == k) {
-                list_v = b;
-                list_i = at;
-            }
+                }
+        }
+        if (lane == k) {
+            list_v = b;
+            list_i = at;
         }
     }
     return r;
 }
 
-// The lists of n <= 32 parts, part q's entries at v[q * 32 .. q * 32 + 32), in order
-// of their numbers where values are equal; lane k gets the k-th of all.
-__device__ __forceinline__ void merge_lists(const float* v, const int* at, int n, int top, float& list_v, int& list_i) {
+// n <= 32 sorted lists merged: lane k gets the k-th entry of all, equal ones by number.
+__device__ __forceinline__ void merge_lists(const Candidates* lists, int n, int top, float& list_v, int& list_i) {
     const int lane = threadIdx.x & 31;
     int next = 0;
-    float head_v = lane < n ? v[lane * 32] : -INFINITY;
-    int head_i = lane < n ? at[lane * 32] : INT_MAX;
+    float head_v = lane < n ? lists[lane].v[0] : -INFINITY;
+    int head_i = lane < n ? lists[lane].i[0] : INT_MAX;
     list_v = -INFINITY;
     for (int k = 0; k < top; ++k) {
         const uint32_t key = ranked(head_v), most = __reduce_max_sync(kAll, key);
@@ -183,8 +269,8 @@ __device__ __forceinline__ void merge_lists(const float* v, const int* at, int n
         }
         if (key == most && head_i == win) {
             ++next;
-            head_v = next < 32 ? v[lane * 32 + next] : -INFINITY;
-            head_i = next < 32 ? at[lane * 32 + next] : INT_MAX;
+            head_v = next < 32 ? lists[lane].v[next] : -INFINITY;
+            head_i = next < 32 ? lists[lane].i[next] : INT_MAX;
         }
     }
 }
@@ -229,24 +315,23 @@ __device__ __forceinline__ const float* row_of(const LogprobParams& p, size_t it
 
 template <int NV>
 __global__ void __launch_bounds__(kShortWarps * 32) logprobs_short_kernel(const LogprobParams p, int items) {
+    __shared__ Candidates cand[kShortWarps];
     const int item = blockIdx.x * kShortWarps + (threadIdx.x >> 5);
     if (item >= items) return;
     const float* z = row_of(p, item);
     float list_v = -INFINITY;
     int list_i = 0;
-    const Part r = warp_run<NV>(z, p.V, 0, kLog2e * p.inv_t, p.top, list_v, list_i);
+    const Part r = warp_run<NV>(z, p.V, 0, kLog2e * p.inv_t, p.top, cand[threadIdx.x >> 5], list_v, list_i);
     finish(p, item, z, r, list_v, list_i);
 }
 
 // A cluster of gridDim.y blocks a row: its warps take runs of the row in turn.
 __global__ void __launch_bounds__(kLongWarps * 32) logprobs_long_kernel(const LogprobParams p) {
     __shared__ Part parts[kLongWarps];
-    __shared__ float lists_v[kLongWarps][32];
-    __shared__ int lists_i[kLongWarps][32];
+    __shared__ Candidates lists[kLongWarps];  // a warp's gathered entries, then its list
     // what the cluster's blocks hand to its first
     __shared__ Part block_part[8];
-    __shared__ float block_v[8][32];
-    __shared__ int block_i[8][32];
+    __shared__ Candidates block_list[8];
     namespace cg = cooperative_groups;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5, C = gridDim.y;
     if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // all blocks run: awaited below
@@ -257,30 +342,30 @@ __global__ void __launch_bounds__(kLongWarps * 32) logprobs_long_kernel(const Lo
     float list_v = -INFINITY;
     int list_i = 0;
     for (int first = ((int)blockIdx.y * W + warp) * kRun; first < p.V; first += C * W * kRun)
-        r = join(r, warp_run<kRunNv>(z + first, min(kRun, p.V - first), first, c, p.top, list_v, list_i), c);
+        r = join(r, warp_run<kRunNv>(z + first, min(kRun, p.V - first), first, c, p.top, lists[warp], list_v, list_i), c);
     if (lane == 0) parts[warp] = r;
-    lists_v[warp][lane] = list_v;
-    lists_i[warp][lane] = list_i;
+    lists[warp].v[lane] = list_v;
+    lists[warp].i[lane] = list_i;
     if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     __syncthreads();
     if (warp == 0) {
         r = join_lanes(lane < W ? parts[lane] : Part{-INFINITY, 0.f, 0.f, 0}, c);
-        merge_lists(&lists_v[0][0], &lists_i[0][0], W, p.top, list_v, list_i);
+        merge_lists(lists, W, p.top, list_v, list_i);
         if (C == 1) {
             finish(p, item, z, r, list_v, list_i);
         } else {
             const auto cluster = cg::this_cluster();
             const unsigned at = blockIdx.y;
             if (lane == 0) *cluster.map_shared_rank(&block_part[at], 0) = r;
-            *cluster.map_shared_rank(&block_v[at][lane], 0) = list_v;
-            *cluster.map_shared_rank(&block_i[at][lane], 0) = list_i;
+            *cluster.map_shared_rank(&block_list[at].v[lane], 0) = list_v;
+            *cluster.map_shared_rank(&block_list[at].i[lane], 0) = list_i;
         }
     }
     if (C == 1) return;
     cg::this_cluster().sync();
     if (blockIdx.y != 0 || warp != 0) return;
     r = join_lanes(lane < C ? block_part[lane] : Part{-INFINITY, 0.f, 0.f, 0}, c);
-    merge_lists(&block_v[0][0], &block_i[0][0], C, p.top, list_v, list_i);
+    merge_lists(block_list, C, p.top, list_v, list_i);
     finish(p, item, z, r, list_v, list_i);
 }
 
