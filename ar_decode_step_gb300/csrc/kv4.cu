@@ -1050,9 +1050,15 @@ extern "C" int tts_attention_decode_kv4(const float* qkv, const void* q_norm, co
     p.max_pos = max_pos;
     p.pos = pos;
     p.eps = eps;
+    // theta^(-i/64) from its square roots' products (a few ulp of fp64; 64 calls of
+    // pow would take longer than the launch)
+    double freq[kHeadDim / 2];
+    freq[0] = 1.0;
+    freq[1] = std::pow((double)rope_theta, -2.0 / (double)kHeadDim);
+    for (int i = 2; i < kHeadDim / 2; ++i) freq[i] = freq[i / 2] * freq[i - i / 2];
     for (int i = 0; i < kHeadDim / 2; ++i) {
-        const double ang = (double)pos * std::pow((double)rope_theta, -2.0 * i / (double)kHeadDim);
-        const double c = std::cos(ang), sn = std::sin(ang);
+        double c, sn;
+        sincos((double)pos * freq[i], &sn, &c);
         p.rope.cs[i] = make_float2((float)c, (float)sn);
         p.rope.rest[i] = make_float2((float)(c - (double)(float)c), (float)(sn - (double)(float)sn));
     }
