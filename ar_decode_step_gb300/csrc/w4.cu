@@ -4,9 +4,11 @@
 // Format: W4 uint8 [N][K/2], low nibble = even k, u in 0..15; s bf16
 // [N][K/128]; weight = s * (u - 8).
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <mutex>
+
+#include <cooperative_groups.h>
 
 #include "kernels.h"
 #include "tts_decode.h"
@@ -18,14 +20,6 @@ constexpr int kW4Group = 128;
 constexpr int kW4MaxM = 8;
 constexpr int kW4MaxK = 12288;
 
-__device__ __forceinline__ void cp_async16_at(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-// 4 bytes of which the last two may be left out (read as zero)
-__device__ __forceinline__ void cp_async4_at(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 struct W4Params {
     const float* x;
     const uint8_t* W4;
@@ -65,7 +59,7 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const __nv_bfloat16* _
 
 // ---- the product -----------------------------------------------------------------
 // y[m][n] = sum_k a[m][k] s[n][k/128] (u[n][k] - 8).  Its time is the reading of
-// the weights once (at most 8 flops a byte), so everything else has to stay
+// the weights once (at most 16 flops a byte), so everything else has to stay
 // below that: a weight may cost about 2.7 of an SM's lane instructions.
 //
 // Codes are the A operand of m16n8k16 products (fp16, fp32 sums) as they lie
@@ -74,25 +68,30 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const __nv_bfloat16* _
 // costs half an instruction and no conversion; q u + q' u' = (q - q'/16) u +
 // (q'/16)(u + 16 u') moves the rest to the activations.  These are the B
 // operand: fp32, scaled per 128 group by a power of two to below 2^15 and split
-// into two fp16 parts (22 bits, and 2^-39 of the group's largest), columns 2m and
-// 2m + 1 for vector m, so up to four vectors cost what one does.  Group sums
-// leave the tensor core once a group and are scaled and added in fp32:
-// acc += s (2^24-e part - 8 sum(a)).
+// into two fp16 parts (22 bits, and 2^-39 of the group's largest).  Up to four
+// vectors take columns 2m and 2m + 1 of one product, eight a product for each
+// part.  Group sums leave the tensor core once a group and are scaled and added
+// in fp32: acc += s (2^(24-e) part - 8 sum(a)).
 //
-// A block takes tiles of 16 rows (epi 2: a gate and an up tile), about one block
-// an SM; its warps take one slice of the groups each, the same for all its
-// tiles, so a warp prepares its slice of the activations once and for itself.
-// A lane copies exactly the 2 x 16 bytes of a group that it uses (rows r and
-// r + 8, piece t), asynchronously into a ring of its own: no barrier before all
-// of a block's tiles are done and the warps' sums are added.
-// (Four small blocks an SM were measured first: gate/up at one vector took
-// 11.7 us, most of it preparing the same activations four times.)
+// About one block an SM.  A block takes tiles of 16 rows (epi 2: a gate and an up
+// tile) of all of K, or of a share of K where its activations or its tiles would
+// not fit the SM (a cluster of blocks then adds up through distributed shared
+// memory).  All its rows are copied at once by the bulk-copy engine, one copy a
+// row, to rows 64 bytes apart modulo 128, so that the 16-byte reads of eight
+// lanes (two rows, four pieces) touch every bank once; a barrier a tile says
+// when it is there, and nothing is ever overwritten.  A warp has one slice of
+// the groups for all tiles, so it prepares its slice of the activations once and
+// for itself, while the first rows are on their way; the warps' sums are added
+// at the end.
+// (Measured first, gate/up at one vector: small blocks, four an SM, 11.7 us, most
+// of it preparing the same activations four times; 16-byte asynchronous copies by
+// the lanes, 10.9 us, of which 3 us to issue them: 40 cache lines an item.)
 constexpr int kMaxTiles = 8;  // tiles (epi 2: pairs) a block, at most
-constexpr int kStage = 1024 + 64;  // an item (tile, group): codes, then a word with each row's scale
 
 struct W4Launch {
-    int warps, tiles, slice;  // tiles a block and groups a warp, at most
+    int warps, tiles, share, log_split;  // tiles a block, groups of K a block at most, log2 of the blocks that share K
     int grid;
+    unsigned long long magic;  // ceil(2^32 / warps): n / warps = n magic >> 32 for the small n here
     size_t smem;
 };
 
@@ -106,102 +105,127 @@ __device__ __forceinline__ void mma16816_f16(float c[4], uint32_t a0, uint32_t a
 __device__ __forceinline__ uint32_t even_bytes(uint32_t w) { return w & 0x00ff00ffu; }
 __device__ __forceinline__ uint32_t odd_bytes(uint32_t w) { return __byte_perm(w, 0u, 0x4341u); }
 
-// Shared memory of a warp: [ring][activations: slice x 4 words x 2 MV columns x
-// 4 pieces x 16 bytes][per group and vector: (2^24 over its power of two, 8 sum)].
-// Then the block's: [sums: tiles x parts x 16 rows x MV x warps][sums of squares].
-__host__ __device__ constexpr int act_group_bytes(int mv) { return 4 * 2 * mv * 4 * 16; }
-__host__ __device__ inline size_t warp_bytes(int mv, int ring, int slice) {
-    return ((size_t)ring * kStage + (size_t)slice * (act_group_bytes(mv) + mv * 8) + 15) & ~(size_t)15;
+// Shared memory of a block: [rows: tiles x parts x 16][activations: share x 4 words
+// x columns x 4 pieces x 16 bytes][per group and vector: (2^24 over its power of
+// two, 8 sum)][scales: tiles x parts x share x 16 bf16][sums: outputs x parts x
+// warps][sums of squares: MV x warps][totals of the block: outputs x parts, MV].
+__host__ __device__ constexpr int columns_of(int mv) { return 2 * mv; }
+__host__ __device__ constexpr int act_group_bytes(int mv) { return 4 * columns_of(mv) * 64; }
+__host__ __device__ constexpr int max_warps(int mv) { return mv >= 4 ? 16 : 24; }
+__host__ __device__ inline int row_pitch(int share) { return share * 64 + (share & 1 ? 0 : 64); }
+struct W4Smem {
+    uint32_t act, par, scales, sums, sq, tot, total;
+};
+__host__ __device__ inline W4Smem smem_of(int mv, int parts, int tiles, int share, int warps) {
+    W4Smem o;
+    const uint32_t outs = tiles * 16 * mv * parts;
+    o.act = tiles * parts * 16 * row_pitch(share);
+    o.par = o.act + share * act_group_bytes(mv);
+    o.scales = o.par + share * mv * 8;
+    o.sums = o.scales + tiles * parts * share * 32;
+    o.sq = o.sums + outs * warps * 4;
+    o.tot = o.sq + mv * warps * 4;
+    o.total = o.tot + (outs + mv) * 4;
+    return o;
 }
-__host__ __device__ constexpr int max_warps(int mv) { return mv == 4 ? 16 : 24; }
 
-template <int MV, int PARTS, int RING>  // vectors a block (1, 2, 4), tiles an output tile takes, items in flight a warp
+template <int MV, int PARTS>  // vectors (1, 2, 4, 8), tiles an output tile takes
 __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4Params p, const W4Launch c) {
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t bars[kMaxTiles * PARTS];
+    __shared__ int late;  // a tile did not arrive: the outputs are NaN
+    constexpr int kVecs = MV == 8 ? 2 : 1;  // vectors a lane adds up
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = c.warps;
     const int r = lane >> 2, t = lane & 3;
-    const int groups = p.K / kW4Group;
-    const int g0 = groups * warp / W, ng = groups * (warp + 1) / W - g0;  // at least 1: W <= groups
-    const int m0 = blockIdx.y * MV, mv = min(MV, p.M - m0);
+    const int groups = p.K / kW4Group, rank = blockIdx.z, split = 1 << c.log_split;
+    const int k0 = groups * rank >> c.log_split, kg = (groups * (rank + 1) >> c.log_split) - k0;  // this block's groups of K
+    const int g0 = (int)(kg * warp * c.magic >> 32), g1 = (int)(kg * (warp + 1) * c.magic >> 32);  // this warp's of those
     const int ntiles = (p.N + 15) / 16;
     const int tile0 = blockIdx.x, step = gridDim.x;
-    const int nt = (ntiles - tile0 + step - 1) / step;  // this block's tiles: tile0, tile0 + step, ...
+    // this block's tiles: tile0, tile0 + step, ...
+    const int nt = c.tiles - ((long long)tile0 + (long long)(c.tiles - 1) * step >= ntiles);
+    const int pitch = row_pitch(c.share);
+    const W4Smem o = smem_of(MV, PARTS, c.tiles, c.share, W);
 
-    uint8_t* mine = smem + (size_t)warp * warp_bytes(MV, RING, c.slice);
-    uint8_t* act = mine + RING * kStage;
-    float2* act_par = reinterpret_cast<float2*>(act + c.slice * act_group_bytes(MV));
-    float* sums = reinterpret_cast<float*>(smem + (size_t)W * warp_bytes(MV, RING, c.slice));
-    float* sq = sums + (size_t)c.tiles * PARTS * 16 * MV * W;  // [MV][W]
-
-    // ---- activations of the slice's first group: before the copies, which would
-    // hold them up
+    // ---- activations of the slice's first group, then the copies
     float4 xs[MV];
     uint2 gb = {};
     auto load_x = [&](int g) {
-        const size_t k = (size_t)(g0 + g) * kW4Group + 4 * lane;
+        const size_t k = (size_t)(k0 + g) * kW4Group + 4 * lane;
 #pragma unroll
         for (int m = 0; m < MV; ++m)
-            xs[m] = m < mv ? *reinterpret_cast<const float4*>(p.x + (size_t)(m0 + m) * p.K + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+            xs[m] = m < p.M ? *reinterpret_cast<const float4*>(p.x + (size_t)m * p.K + k) : make_float4(0.f, 0.f, 0.f, 0.f);
         if (p.gamma) gb = *reinterpret_cast<const uint2*>(p.gamma + k);
     };
-    load_x(0);
-
-    // ---- copies, item by item: tile, part of it, group
-    const uint32_t ring = smem_u32(mine);
-    const long long total = (long long)p.N * PARTS * groups;  // scales in all
-    int iq = 0, ig = 0;                                       // next item to copy
-    const uint8_t *pa = nullptr, *pb = nullptr;
-    long long ps = 0;
+    if (g0 < g1) load_x(g0);
+    if (threadIdx.x == 0) {
+        for (int q = 0; q < nt * PARTS; ++q) mbar_init(&bars[q], 1);
+        late = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     // row i of the block's tile q; past the end the last row, whose result is not
     // stored
     auto row_of = [&](int q, int i) {
-        const int tile = tile0 + (q / PARTS) * step;
-        return min(tile * 16 + i, p.N - 1) + (q % PARTS) * p.N;
+        return min((tile0 + q / PARTS * step) * 16 + i, p.N - 1) + (q % PARTS) * p.N;
     };
-    auto issue = [&](int stage) {
-        if (iq >= nt * PARTS) return;
-        if (ig == 0) {
-            pa = p.W4 + (size_t)row_of(iq, r) * (p.K / 2) + (size_t)g0 * 64 + t * 16;
-            pb = p.W4 + (size_t)row_of(iq, r + 8) * (p.K / 2) + (size_t)g0 * 64 + t * 16;
-            ps = (long long)row_of(iq, lane & 15) * groups + g0;
-        }
-        const uint32_t dst = ring + stage * kStage;
-        cp_async16_at(dst + lane * 16, pa + ig * 64);
-        cp_async16_at(dst + 512 + lane * 16, pb + ig * 64);
-        // the 4-byte word that holds the row's scale; the last one of all may be
-        // half a word
-        const long long at = (ps + ig) & ~1ll;
-        if (lane < 16) cp_async4_at(dst + 1024 + lane * 4, p.s + at, at + 1 < total ? 4 : 2);
-        if (++ig == ng) {
-            ig = 0;
-            ++iq;
-        }
-    };
+    // scales, a row a warp at a time, eight rows in flight; the first before the
+    // copies, which would hold them up for 2 us
+    __nv_bfloat16* scl = reinterpret_cast<__nv_bfloat16*>(smem + o.scales);
+    constexpr int kAhead = 8;
+    const int rows = nt * PARTS * 16;
+    __nv_bfloat16 sv[kAhead];
+    auto load_scales = [&](int i0, int gl) {
 #pragma unroll
-    for (int i = 0; i < RING - 1; ++i) {
-        issue(i);
-        cp_async_commit_group();
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = min(i0 + j * W, rows - 1);  // past the end the last row again
+            if (gl < kg) sv[j] = p.s[(size_t)row_of(i >> 4, i & 15) * groups + k0 + gl];
+        }
+    };
+    auto keep_scales = [&](int i0, int gl) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int i = i0 + j * W;
+            if (i < rows && gl < kg) scl[((i >> 4) * c.share + gl) * 16 + (i & 15)] = sv[j];
+        }
+    };
+    load_scales(warp, lane);
+    for (int q = warp; q < nt * PARTS; q += W) {
+        if (lane == 0) mbar_arrive_expect_tx(&bars[q], 16 * kg * 64);
+        __syncwarp();
+        if (lane < 16)
+            bulk_g2s(smem + (size_t)(q * 16 + lane) * pitch, p.W4 + (size_t)row_of(q, lane) * (p.K / 2) + k0 * 64, kg * 64,
+                     &bars[q], l2_evict_first_policy());
     }
+    keep_scales(warp, lane);
+    for (int gl = lane; gl < kg; gl += 32)
+        for (int i0 = gl == lane ? warp + kAhead * W : warp; i0 < rows; i0 += kAhead * W) {
+            load_scales(i0, gl);
+            keep_scales(i0, gl);
+        }
 
-    // half-warp h of the block adds up output h, h + 2 W, ... at the end: what it
+    // a thread adds up output i = its number, + threads, ... at the end: what it
     // adds the first of them to
-    const int half = threadIdx.x >> 4, h_lane = threadIdx.x & 15;
+    const int outs = nt * 16 * MV;
     auto place = [&](int i, size_t* at) {  // output i: (tile, row, vector)
         const int n = (tile0 + i / (16 * MV) * step) * 16 + (i / MV) % 16, m = i % MV;
-        *at = (size_t)(m0 + m) * p.N + n;
-        return i < nt * 16 * MV && n < p.N && m < mv;
+        *at = (size_t)m * p.N + n;
+        return i < outs && n < p.N && m < p.M;
     };
     float resid = 0.f;
-    if (p.resid && h_lane == 0) {
+    if (p.resid && split == 1) {
         size_t at;
-        if (place(half, &at)) resid = p.resid[at];
+        if (place(threadIdx.x, &at)) resid = p.resid[at];
     }
 
     // ---- this warp's slice of the activations
+    float2* act_par = reinterpret_cast<float2*>(smem + o.par);
+    float* sq = reinterpret_cast<float*>(smem + o.sq);  // [W][MV]
     float ss[MV];
 #pragma unroll
     for (int m = 0; m < MV; ++m) ss[m] = 0.f;
-    for (int g = 0; g < ng; ++g) {
+    for (int g = g0; g < g1; ++g) {
         float a[MV][4];
 #pragma unroll
         for (int m = 0; m < MV; ++m) {
@@ -218,8 +242,9 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
                 a[m][3] *= bf16hi(gb.y);
             }
         }
-        if (g + 1 < ng) load_x(g + 1);
-        uint8_t* dst = act + (size_t)g * act_group_bytes(MV) + ((lane >> 1) & 3) * (2 * MV * 64) + (lane >> 3) * 16 + (lane & 1) * 8;
+        if (g + 1 < g1) load_x(g + 1);
+        uint8_t* dst = smem + o.act + (size_t)g * act_group_bytes(MV) + ((lane >> 1) & 3) * (columns_of(MV) * 64) +
+                       (lane >> 3) * 16 + (lane & 1) * 8;
 #pragma unroll
         for (int m = 0; m < MV; ++m) {
             const float sum = warp_sum((a[m][0] + a[m][1]) + (a[m][2] + a[m][3]));
@@ -248,146 +273,225 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
             const uint32_t gl = __shfl_xor_sync(0xffffffffu, odd ? lo[0] : lo[1], 1);
             const uint32_t eh = odd ? gh : hi[0], oh = odd ? hi[1] : gh;  // the even and the odd lane's halves
             const uint32_t el = odd ? gl : lo[0], ol = odd ? lo[1] : gl;
-            *reinterpret_cast<uint2*>(dst + 2 * m * 64) = make_uint2(__byte_perm(eh, oh, 0x5410), __byte_perm(eh, oh, 0x7632));
-            *reinterpret_cast<uint2*>(dst + 2 * m * 64 + 64) = make_uint2(__byte_perm(el, ol, 0x5410), __byte_perm(el, ol, 0x7632));
+            uint8_t* d = dst + (MV == 8 ? m : 2 * m) * 64;
+            *reinterpret_cast<uint2*>(d) = make_uint2(__byte_perm(eh, oh, 0x5410), __byte_perm(eh, oh, 0x7632));
+            *reinterpret_cast<uint2*>(d + (MV == 8 ? 512 : 64)) = make_uint2(__byte_perm(el, ol, 0x5410), __byte_perm(el, ol, 0x7632));
         }
     }
     if (p.gamma) {
 #pragma unroll
         for (int m = 0; m < MV; ++m) {
             ss[m] = warp_sum(ss[m]);
-            if (lane == 0) sq[m * W + warp] = ss[m];
+            if (lane == 0) sq[warp * MV + m] = ss[m];
         }
     }
-    __syncwarp();
+    __syncthreads();  // the scales come from other warps
 
-    // ---- the products
-    int stage = 0, fill = RING - 1;
-    const bool column = r < 2 * MV;
-    const uint8_t* my_act = act + r * 64 + t * 16;
-    for (int q = 0; q < nt * PARTS; ++q) {
-        float acc[2] = {0.f, 0.f};
-        // which half of its word a row's first scale is
-        const int oa = (row_of(q, r) & groups & 1) ^ (g0 & 1), ob = (row_of(q, r + 8) & groups & 1) ^ (g0 & 1);
-        for (int g = 0; g < ng; ++g) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(RING - 2) : "memory");
-            __syncwarp();  // the scales come through other lanes' copies
-            issue(fill);
-            cp_async_commit_group();
-            if (++fill == RING) fill = 0;
-            const uint8_t* st = mine + stage * kStage;
-            if (++stage == RING) stage = 0;
-            const uint4 wa = *reinterpret_cast<const uint4*>(st + lane * 16);
-            const uint4 wb = *reinterpret_cast<const uint4*>(st + 512 + lane * 16);
-            const uint32_t sa = *reinterpret_cast<const uint32_t*>(st + 1024 + r * 4);
-            const uint32_t sb = *reinterpret_cast<const uint32_t*>(st + 1024 + r * 4 + 32);
+    // ---- the products: a group's activations in registers, all tiles past them
+    float* sums = reinterpret_cast<float*>(smem + o.sums) + (size_t)warp * outs * PARTS;  // [W][tile x parts][row][vector]
+    const bool column = MV == 8 || r < 2 * MV;
+    for (int g = g0; g < g1; ++g) {
+        uint4 b[kVecs][4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const uint8_t* at = smem + o.act + (size_t)g * act_group_bytes(MV) + w * (columns_of(MV) * 64) + r * 64 + t * 16;
+            b[0][w] = column ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
+            if (MV == 8) b[kVecs - 1][w] = *reinterpret_cast<const uint4*>(at + 512);
+        }
+        float2 ap[kVecs];
+#pragma unroll
+        for (int v = 0; v < kVecs; ++v) ap[v] = act_par[g * MV + min(kVecs * t + v, MV - 1)];
+        const uint8_t* row = smem + r * pitch + t * 16 + g * 64;
+        const __nv_bfloat16* sc = scl + g * 16 + r;
+        float* out = sums + r * MV + kVecs * t;
+        for (int q = 0; q < nt * PARTS; ++q) {
+            if (g == g0 && !mbar_wait(&bars[q], 0)) late = 1;
+            const uint4 wa = *reinterpret_cast<const uint4*>(row);
+            const uint4 wb = *reinterpret_cast<const uint4*>(row + 8 * pitch);
+            const float sa = __bfloat162float(sc[0]), sb = __bfloat162float(sc[8]);
+            row += 16 * pitch;
+            sc += 16 * c.share;
             const uint32_t ua[4] = {wa.x, wa.y, wa.z, wa.w}, ub[4] = {wb.x, wb.y, wb.z, wb.w};
             float d[2][4] = {};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                uint4 b = make_uint4(0, 0, 0, 0);
-                if (column) b = *reinterpret_cast<const uint4*>(my_act + (size_t)g * act_group_bytes(MV) + w * (2 * MV * 64));
                 const uint32_t x0 = even_bytes(ua[w]), y0 = even_bytes(ub[w]), x1 = odd_bytes(ua[w]), y1 = odd_bytes(ub[w]);
-                mma16816_f16(d[0], x0 & 0x000f000fu, y0 & 0x000f000fu, x0, y0, b.x, b.y);
-                mma16816_f16(d[1], x1 & 0x000f000fu, y1 & 0x000f000fu, x1, y1, b.z, b.w);
+                const uint32_t xl0 = x0 & 0x000f000fu, yl0 = y0 & 0x000f000fu, xl1 = x1 & 0x000f000fu, yl1 = y1 & 0x000f000fu;
+#pragma unroll
+                for (int v = 0; v < kVecs; ++v) {
+                    mma16816_f16(d[0], xl0, yl0, x0, y0, b[v][w].x, b[v][w].y);
+                    mma16816_f16(d[1], xl1, yl1, x1, y1, b[v][w].z, b[v][w].w);
+                }
             }
-            const float2 ap = act_par[g * MV + (t < MV ? t : 0)];
-            const float va = (d[0][0] + d[1][0]) + (d[0][1] + d[1][1]), vb = (d[0][2] + d[1][2]) + (d[0][3] + d[1][3]);
-            acc[0] = fmaf((g ^ oa) & 1 ? bf16hi(sa) : bf16lo(sa), fmaf(va, ap.x, -ap.y), acc[0]);
-            acc[1] = fmaf((g ^ ob) & 1 ? bf16hi(sb) : bf16lo(sb), fmaf(vb, ap.x, -ap.y), acc[1]);
-        }
-        if (t < MV) {
-            float* s = sums + (size_t)(q * 16 * MV + t) * W + warp;
-            s[(size_t)r * MV * W] = acc[0];
-            s[(size_t)(r + 8) * MV * W] = acc[1];
+            if (MV == 8) {
+#pragma unroll
+                for (int v = 0; v < kVecs; ++v) {
+                    const float ya = sa * fmaf(d[0][v] + d[1][v], ap[v].x, -ap[v].y);
+                    const float yb = sb * fmaf(d[0][2 + v] + d[1][2 + v], ap[v].x, -ap[v].y);
+                    out[v] = g == g0 ? ya : out[v] + ya;
+                    out[8 * MV + v] = g == g0 ? yb : out[8 * MV + v] + yb;
+                }
+            } else if (t < MV) {
+                const float ya = sa * fmaf((d[0][0] + d[1][0]) + (d[0][1] + d[1][1]), ap[0].x, -ap[0].y);
+                const float yb = sb * fmaf((d[0][2] + d[1][2]) + (d[0][3] + d[1][3]), ap[0].x, -ap[0].y);
+                out[0] = g == g0 ? ya : out[0] + ya;
+                out[8 * MV] = g == g0 ? yb : out[8 * MV] + yb;
+            }
+            out += 16 * MV;
         }
     }
+    if (g0 == g1)  // no group: nothing of this warp's, but its copies
+        for (int i = lane; i < outs * PARTS; i += 32) sums[i] = 0.f;
+    for (int q = 0; q < nt * PARTS; ++q)
+        if (g0 == g1 && !mbar_wait(&bars[q], 0)) late = 1;
     __syncthreads();
 
-    // ---- the warps' sums, an output a half-warp, and the epilogue
-    auto half_sum = [&](const float* v) {  // of W values, in a fixed order
-        float s = h_lane < W ? v[h_lane] : 0.f;
-        if (h_lane + 16 < W) s += v[h_lane + 16];
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        return s;
+    // ---- the warps' sums in order, an output a thread
+    const float* all = reinterpret_cast<const float*>(smem + o.sums);
+    float* tot = reinterpret_cast<float*>(smem + o.tot);  // [MV] squares, [tile][part][row][vector]
+    auto store = [&](size_t at, float v0, float v1, float squares, float add) {
+        const float rms = p.gamma ? 1.f / sqrtf(squares / (float)p.K + p.eps) : 1.f;
+        float y = v0 * rms + add;
+        if (PARTS == 2) y = y / (1.f + expf(-y)) * (v1 * rms);
+        p.y[at] = late ? NAN : y;
     };
-    const int outs = nt * 16 * MV;
-    for (int i0 = 0; i0 < outs; i0 += 2 * W) {
-        const int i = i0 + half, at_i = min(i, outs - 1);
-        const int q = at_i / (16 * MV), rest = at_i % (16 * MV);
-        float v[PARTS], rms = 1.f;
+    for (int i = threadIdx.x; i < outs; i += W * 32) {
+        const int first = i + i / (16 * MV) * (16 * MV) * (PARTS - 1);  // part 0 of output i
+        float v[PARTS] = {}, squares = 0.f;
+#pragma unroll 4
+        for (int w = 0; w < W; ++w) {
 #pragma unroll
-        for (int h = 0; h < PARTS; ++h) v[h] = half_sum(sums + (size_t)((q * PARTS + h) * 16 * MV + rest) * W);
-        if (p.gamma) rms = 1.f / sqrtf(half_sum(sq + (at_i % MV) * W) / (float)p.K + p.eps);
-        size_t at;
-        if (place(i, &at) && h_lane == 0) {
-            float y = v[0] * rms;
-            if (p.resid) y += i0 == 0 ? resid : p.resid[at];
-            if (PARTS == 2) y = y / (1.f + expf(-y)) * (v[PARTS - 1] * rms);
-            p.y[at] = y;
+            for (int h = 0; h < PARTS; ++h) v[h] += all[(size_t)w * outs * PARTS + first + h * 16 * MV];
+            if (p.gamma) squares += sq[w * MV + i % MV];
+        }
+        if (split == 1) {
+            size_t at;
+            if (place(i, &at)) store(at, v[0], v[PARTS - 1], squares, p.resid ? (i < W * 32 ? resid : p.resid[at]) : 0.f);
+        } else {
+            if (i < MV) tot[i] = squares;
+#pragma unroll
+            for (int h = 0; h < PARTS; ++h) tot[MV + first + h * 16 * MV] = v[h];
         }
     }
+    if (split == 1) return;
+
+    // ---- the blocks' totals, outputs in turn by the blocks of the cluster
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // all blocks run
+    const auto cluster = cooperative_groups::this_cluster();
+    cluster.sync();
+    for (int i = (int)threadIdx.x * split + rank; i < outs; i += W * 32 * split) {
+        const int first = i + i / (16 * MV) * (16 * MV) * (PARTS - 1);
+        float v[PARTS] = {}, squares = 0.f;
+        for (int k = 0; k < split; ++k) {
+            const float* theirs = cluster.map_shared_rank(tot, k);
+            squares += theirs[i % MV];
+#pragma unroll
+            for (int h = 0; h < PARTS; ++h) v[h] += theirs[MV + first + h * 16 * MV];
+        }
+        size_t at;
+        if (place(i, &at)) store(at, v[0], v[PARTS - 1], squares, p.resid ? p.resid[at] : 0.f);
+    }
+    cluster.sync();  // before a block's shared memory goes
 }
 
-constexpr size_t kBlockSmem = 227 * 1024;
+constexpr size_t kBlockSmem = 227 * 1024 - 1024;  // the barriers' share left out
 
-// Blocks, warps a block and tiles a block for p at MV vectors a block; ring is
-// set to the copies in flight a warp.
-W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, int ny, int sms, int* ring) {
+// Blocks, warps a block, tiles a block and the split of K for p at MV vectors;
+// at_once[i]: clusters of 2^i blocks of this kernel that run at once.
+W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, const int at_once[4]) {
     const int groups = p.K / kW4Group, ntiles = (p.N + 15) / 16;
-    // a block an SM, which takes its tiles one after another
-    int grid = std::min(ntiles, std::max(1, sms / ny));
-    grid = std::max(grid, (ntiles + kMaxTiles - 1) / kMaxTiles);
-    const int tiles = (ntiles + grid - 1) / grid;
-    W4Launch best{};
-    int best_cost = 1 << 30;
-    for (const int rg : {8, 3})
-        for (int w = std::min(groups, max_warps(mv)); w >= 1; --w) {
-            const int slice = (groups + w - 1) / w;
-            const size_t smem = w * warp_bytes(mv, rg, slice) + 4 * (size_t)w * mv * (tiles * parts * 16 + 1);
-            if (smem > kBlockSmem) continue;
-            // items of a tile that the fullest scheduler issues; under 12 warps
-            // they wait for one another more
-            const int cost = (w + 3) / 4 * slice * (w >= 12 ? 4 : 5);
+    auto warps_for = [&](int share) {
+        // a group takes a scheduler about 90 cycles of issue and a warp about 400 from
+        // load to sum: the count with the shortest tile, ties to more warps
+        int best = 1, best_cost = 1 << 30;
+        for (int w = std::min(share, max_warps(mv)); w >= 1; --w) {
+            const int cost = (share + w - 1) / w * std::max(2 * ((w + 3) / 4), 9);
             if (cost < best_cost) {
                 best_cost = cost;
-                best = W4Launch{w, tiles, slice, grid, smem};
-                *ring = rg;
+                best = w;
             }
         }
-    return best;
-}
-
-template <int MV, int PARTS, int RING>
-cudaError_t launch_gemv_w4_as(const W4Params& p, const W4Launch& c, int ny, int dev, cudaStream_t s) {
-    static std::atomic<unsigned long long> ready{0};  // devices whose shared-memory limit is raised
-    const unsigned long long bit = 1ull << (dev & 63);
-    const auto kern = gemv_w4_kernel<MV, PARTS, RING>;
-    if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBlockSmem);
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(bit, std::memory_order_relaxed);
+        return best;
+    };
+    auto made = [&](int log_split, int tiles, int grid) {
+        const int share = (groups + (1 << log_split) - 1) >> log_split, warps = warps_for(share);
+        return W4Launch{warps, tiles, share, log_split, grid, ((1ull << 32) + warps - 1) / warps,
+                        smem_of(mv, parts, tiles, share, warps).total};
+    };
+    // the least split of K with which all tiles are resident at once, a block an SM
+    for (int ls = 0; ls < 4 && (1 << ls) <= groups; ++ls) {
+        const int most = std::max(1, std::min(ntiles, at_once[ls])), tiles = (ntiles + most - 1) / most;
+        if (tiles > kMaxTiles) continue;
+        const W4Launch c = made(ls, tiles, most);
+        if (c.smem <= kBlockSmem) return c;
     }
-    kern<<<dim3(c.grid, ny), c.warps * 32, c.smem, s>>>(p, c);
-    return cudaGetLastError();
+    // more tiles than that: as many a block as fit, over several rounds of blocks
+    for (int ls = 0; ls < 4 && (1 << ls) <= groups; ++ls)
+        for (int tiles = std::min(kMaxTiles, ntiles); tiles >= 1; --tiles) {
+            const W4Launch c = made(ls, tiles, (ntiles + tiles - 1) / tiles);
+            if (c.smem <= kBlockSmem && (tiles >= 2 || ls == 3 || (2 << ls) > groups)) return c;
+        }
+    return W4Launch{};
 }
 
-template <int MV>
-cudaError_t launch_gemv_w4_mv(const W4Params& p, int dev, int sms, cudaStream_t s) {
-    const int ny = (p.M + MV - 1) / MV;
-    int ring = 0;
-    const W4Launch c = plan_gemv_w4(p, MV, p.epi == 2 ? 2 : 1, ny, sms, &ring);
+template <int MV, int PARTS>
+cudaError_t launch_gemv_w4_as(const W4Params& p, int dev, int sms, cudaStream_t s) {
+    // per device: the shared-memory limit raised, and how many clusters of 1, 2, 4
+    // and 8 blocks run at once with a block an SM (a cluster stays within a group
+    // of SMs, so fewer than SMs / blocks)
+    static std::mutex mu;
+    static int at_once_of[64][4] = {};
+    const auto kern = gemv_w4_kernel<MV, PARTS>;
+    int at_once[4];
+    {
+        const std::lock_guard<std::mutex> lock(mu);
+        int* v = at_once_of[dev & 63];
+        if (!v[0]) {
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBlockSmem);
+            if (e != cudaSuccess) return e;
+            int n[4] = {sms, 0, 0, 0};
+            for (int ls = 1; ls < 4; ++ls) {
+                cudaLaunchConfig_t q = {};
+                q.gridDim = dim3(sms, 1, 1 << ls);
+                q.blockDim = dim3(max_warps(MV) * 32);
+                q.dynamicSmemBytes = kBlockSmem;
+                cudaLaunchAttribute at[1];
+                at[0].id = cudaLaunchAttributeClusterDimension;
+                at[0].val.clusterDim.x = 1;
+                at[0].val.clusterDim.y = 1;
+                at[0].val.clusterDim.z = 1 << ls;
+                q.attrs = at;
+                q.numAttrs = 1;
+                e = cudaOccupancyMaxActiveClusters(&n[ls], kern, &q);
+                if (e != cudaSuccess) return e;
+            }
+            std::copy(n, n + 4, v);
+        }
+        std::copy(v, v + 4, at_once);
+    }
+    const W4Launch c = plan_gemv_w4(p, MV, PARTS, at_once);
     if (!c.warps) return cudaErrorInvalidValue;
-    if (p.epi == 2)
-        return ring == 8 ? launch_gemv_w4_as<MV, 2, 8>(p, c, ny, dev, s) : launch_gemv_w4_as<MV, 2, 3>(p, c, ny, dev, s);
-    return ring == 8 ? launch_gemv_w4_as<MV, 1, 8>(p, c, ny, dev, s) : launch_gemv_w4_as<MV, 1, 3>(p, c, ny, dev, s);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c.grid, 1, 1 << c.log_split);
+    cfg.blockDim = dim3(c.warps * 32);
+    cfg.dynamicSmemBytes = c.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1 << c.log_split;
+    cfg.attrs = at;
+    cfg.numAttrs = c.log_split > 0 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, p, c);
 }
 
 cudaError_t launch_gemv_w4(const W4Params& p, int dev, int sms, cudaStream_t s) {
-    if (p.M == 1) return launch_gemv_w4_mv<1>(p, dev, sms, s);
-    if (p.M == 2) return launch_gemv_w4_mv<2>(p, dev, sms, s);
-    return launch_gemv_w4_mv<4>(p, dev, sms, s);
+    const bool two = p.epi == 2;
+    if (p.M == 1) return two ? launch_gemv_w4_as<1, 2>(p, dev, sms, s) : launch_gemv_w4_as<1, 1>(p, dev, sms, s);
+    if (p.M == 2) return two ? launch_gemv_w4_as<2, 2>(p, dev, sms, s) : launch_gemv_w4_as<2, 1>(p, dev, sms, s);
+    if (p.M <= 4) return two ? launch_gemv_w4_as<4, 2>(p, dev, sms, s) : launch_gemv_w4_as<4, 1>(p, dev, sms, s);
+    return two ? launch_gemv_w4_as<8, 2>(p, dev, sms, s) : launch_gemv_w4_as<8, 1>(p, dev, sms, s);
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
