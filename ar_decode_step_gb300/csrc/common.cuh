@@ -41,6 +41,30 @@ struct alignas(64) DevState {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Host side: launch with such an edge from the kernel before it in the stream.
+// The kernel triggers at its start and waits before its first access to global
+// memory, so its blocks may start as soon as an SM is free while every memory
+// access stays in stream order.  Clusters of cluster_y x cluster_z blocks.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_ordered(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster_y,
+                                  int cluster_z, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 1;
+    at[1].val.clusterDim.y = cluster_y;
+    at[1].val.clusterDim.z = cluster_z;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster_y * cluster_z > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // ---- loads ----------------------------------------------------------------
 // 16-byte streaming load of read-only data that is used once (weights): no L1
 // allocation.  Not volatile, so the compiler may schedule it freely; it must

@@ -110,6 +110,8 @@ __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinter
 __device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 
 __global__ void __launch_bounds__(kRowThreads) quantize_kv4_kernel(const RowParams p) {
+    pdl_trigger();
+    pdl_wait();
     const int head = blockIdx.y >> 1, lane = threadIdx.x & 15, h = lane >> 3, unit = lane & 7;
     const bool is_v = blockIdx.y & 1;
     const int i0 = blockIdx.x * kBlockRows + (threadIdx.x >> 4);
@@ -178,6 +180,8 @@ __global__ void __launch_bounds__(kRowThreads) quantize_kv4_kernel(const RowPara
 }
 
 __global__ void __launch_bounds__(kRowThreads) dequantize_kv4_kernel(const RowParams p) {
+    pdl_trigger();
+    pdl_wait();
     const int head = blockIdx.y >> 1, lane = threadIdx.x & 15, h = lane >> 3, unit = lane & 7;
     const bool is_v = blockIdx.y & 1;
     const int i0 = blockIdx.x * kBlockRows + (threadIdx.x >> 4);
@@ -449,6 +453,23 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
     const size_t base = (size_t)g * p.max_pos;
     const int tile_end = min((p.pos + kTilePos - 1) / kTilePos, (split + 1) * p.tiles_per_split);
 
+    // the angles from the launch parameters to shared memory, an entry a warp at
+    // a time: parameters are read fast at one address a warp only
+    constexpr int kEach = (kHeadDim / 2 + kAttnWarps - 1) / kAttnWarps;
+    float2 cs[kEach], rest[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int at = min(warp + i * kAttnWarps, kHeadDim / 2 - 1);
+        cs[i] = p.rope.cs[at];
+        rest[i] = p.rope.rest[at];
+    }
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kEach; ++i)
+            rope[min(warp + i * kAttnWarps, kHeadDim / 2 - 1)] = make_float4(cs[i].x, cs[i].y, rest[i].x, rest[i].y);
+    }
+    pdl_trigger();
+    pdl_wait();
     // the group's queries, one warp each, and in the last split the new row, its
     // key by the last warp and its value by the one before: their loads first
     const bool new_k = has_new && warp == kAttnWarps - 1, new_v = has_new && warp == kAttnWarps - 2;
@@ -465,21 +486,6 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
     if (next < tile_end) copy.issue(next, 0, lane);
     cp_async_commit();
     next += kAttnWarps;
-    // the angles from the launch parameters to shared memory, an entry a warp at
-    // a time: parameters are read fast at one address a warp only
-    constexpr int kEach = (kHeadDim / 2 + kAttnWarps - 1) / kAttnWarps;
-    float2 cs[kEach], rest[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-        const int at = min(warp + i * kAttnWarps, kHeadDim / 2 - 1);
-        cs[i] = p.rope.cs[at];
-        rest[i] = p.rope.rest[at];
-    }
-    if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < kEach; ++i)
-            rope[min(warp + i * kAttnWarps, kHeadDim / 2 - 1)] = make_float4(cs[i].x, cs[i].y, rest[i].x, rest[i].y);
-    }
     __syncthreads();
     // the other stages' copies only now: before it they held up the loads above
 #pragma unroll
@@ -943,8 +949,7 @@ cudaError_t launch_attn_kv4(const Kv4Params& p, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    attn_kv4_kernel<G><<<p.n_kv * p.S, kAttnWarps * 32, kAttnSmem, s>>>(p);
-    return cudaGetLastError();
+    return launch_ordered(attn_kv4_kernel<G>, dim3(p.n_kv * p.S), dim3(kAttnWarps * 32), kAttnSmem, s, 1, 1, p);
 }
 
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
@@ -993,9 +998,8 @@ extern "C" int tts_quantize_kv4(const void* k, const void* v, int n_kv, int p0, 
                       static_cast<const uint32_t*>(k_par),  static_cast<const uint32_t*>(v_par),
                       static_cast<const uint16_t*>(k),      static_cast<const uint16_t*>(v),
                       p0, p1 - p0, src_stride, max_pos};
-    quantize_kv4_kernel<<<dim3((p.np + kBlockRows - 1) / kBlockRows, 2 * n_kv), kRowThreads, 0,
-                          static_cast<cudaStream_t>(stream)>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_ordered(quantize_kv4_kernel, dim3((p.np + kBlockRows - 1) / kBlockRows, 2 * n_kv),
+                                         dim3(kRowThreads), 0, static_cast<cudaStream_t>(stream), 1, 1, p);
     return e == cudaSuccess ? TTS_OK : report_kv4(e, "tts_quantize_kv4");
 }
 
@@ -1008,9 +1012,8 @@ extern "C" int tts_dequantize_kv4(const void* k4, const void* v4, const void* k_
                       static_cast<const uint32_t*>(k_par),  static_cast<const uint32_t*>(v_par),
                       static_cast<const uint16_t*>(k),      static_cast<const uint16_t*>(v),
                       p0, p1 - p0, dst_stride, max_pos};
-    dequantize_kv4_kernel<<<dim3((p.np + kBlockRows - 1) / kBlockRows, 2 * n_kv), kRowThreads, 0,
-                            static_cast<cudaStream_t>(stream)>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_ordered(dequantize_kv4_kernel, dim3((p.np + kBlockRows - 1) / kBlockRows, 2 * n_kv),
+                                         dim3(kRowThreads), 0, static_cast<cudaStream_t>(stream), 1, 1, p);
     return e == cudaSuccess ? TTS_OK : report_kv4(e, "tts_dequantize_kv4");
 }
 

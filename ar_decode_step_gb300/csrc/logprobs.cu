@@ -317,6 +317,8 @@ template <int NV>
 __global__ void __launch_bounds__(kShortWarps * 32) logprobs_short_kernel(const LogprobParams p, int items) {
     __shared__ Candidates cand[kShortWarps];
     const int item = blockIdx.x * kShortWarps + (threadIdx.x >> 5);
+    pdl_trigger();
+    pdl_wait();
     if (item >= items) return;
     const float* z = row_of(p, item);
     float list_v = -INFINITY;
@@ -335,6 +337,8 @@ __global__ void __launch_bounds__(kLongWarps * 32) logprobs_long_kernel(const Lo
     namespace cg = cooperative_groups;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5, C = gridDim.y;
     if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // all blocks run: awaited below
+    pdl_trigger();
+    pdl_wait();
     const size_t item = blockIdx.x;
     const float* z = row_of(p, item);
     const float c = kLog2e * p.inv_t;
@@ -377,29 +381,15 @@ cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t s) {
         const unsigned grid = (items + kShortWarps - 1) / kShortWarps;
         // 8 values a lane where that is enough: the 33 of a longer run would be
         // mostly padding
-        if (p.V <= 256)
-            logprobs_short_kernel<8><<<grid, kShortWarps * 32, 0, s>>>(p, items);
-        else
-            logprobs_short_kernel<kRunNv><<<grid, kShortWarps * 32, 0, s>>>(p, items);
-        return cudaGetLastError();
+        return launch_ordered(p.V <= 256 ? logprobs_short_kernel<8> : logprobs_short_kernel<kRunNv>, dim3(grid),
+                              dim3(kShortWarps * 32), 0, s, 1, 1, p, items);
     }
     const int runs = (p.V + kRun - 1) / kRun, W = std::min(kLongWarps, runs);
     // one block a row, or so many that every warp has one run, while the rows do
     // not fill the SMs by themselves
     int C = 1;
     while (C < 8 && C * W < runs && (long long)items * C < 152) C *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(items, C);
-    cfg.blockDim = dim3(W * 32);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 1;
-    at[0].val.clusterDim.y = C;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = C > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, logprobs_long_kernel, p);
+    return launch_ordered(logprobs_long_kernel, dim3(items, C), dim3(W * 32), 0, s, C, 1, p);
 }
 
 }  // namespace tts

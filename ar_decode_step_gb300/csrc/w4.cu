@@ -157,7 +157,6 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
             xs[m] = m < p.M ? *reinterpret_cast<const float4*>(p.x + (size_t)m * p.K + k) : make_float4(0.f, 0.f, 0.f, 0.f);
         if (p.gamma) gb = *reinterpret_cast<const uint2*>(p.gamma + k);
     };
-    if (g0 < g1) load_x(g0);
     if (threadIdx.x == 0) {
         for (int q = 0; q < nt * PARTS; ++q) mbar_init(&bars[q], 1);
         late = 0;
@@ -165,6 +164,9 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
     }
     __syncthreads();
     if (split > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    pdl_trigger();
+    pdl_wait();
+    if (g0 < g1) load_x(g0);
     // row i of the block's tile q; past the end the last row, whose result is not
     // stored
     auto row_of = [&](int q, int i) {
@@ -471,19 +473,7 @@ cudaError_t launch_gemv_w4_as(const W4Params& p, int dev, int sms, cudaStream_t 
     }
     const W4Launch c = plan_gemv_w4(p, MV, PARTS, at_once);
     if (!c.warps) return cudaErrorInvalidValue;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(c.grid, 1, 1 << c.log_split);
-    cfg.blockDim = dim3(c.warps * 32);
-    cfg.dynamicSmemBytes = c.smem;
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = 1;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1 << c.log_split;
-    cfg.attrs = at;
-    cfg.numAttrs = c.log_split > 0 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, p, c);
+    return launch_ordered(kern, dim3(c.grid, 1, 1 << c.log_split), dim3(c.warps * 32), c.smem, s, 1, 1 << c.log_split, p, c);
 }
 
 cudaError_t launch_gemv_w4(const W4Params& p, int dev, int sms, cudaStream_t s) {
