@@ -70,17 +70,29 @@ __device__ __forceinline__ Part join_lanes(Part a, float c) {
     return a;
 }
 
-// The `top` (at most 32) largest of up to 32 candidates above -inf, one a lane
-// (cand_v = -inf: none), largest first, equal ones by number: lane k gets the k-th.
-__device__ __forceinline__ void sort_candidates(float cand_v, int cand_i, int top, float& list_v, int& list_i) {
+// Up to 64 candidates for the alternatives; a sorted list of up to 32 uses the first half.
+struct Candidates {
+    float v[64];
+    int i[64];
+};
+// The `top` (at most 32) largest of n <= 64 candidates, all above -inf, largest
+// first, equal ones by number: lane k gets the k-th.
+__device__ __forceinline__ void sort_candidates(const Candidates& c, int n, int top, float& list_v, int& list_i) {
     const int lane = threadIdx.x & 31;
-    uint32_t key = ranked(cand_v);
+    // two a lane, the better one first
+    uint32_t key = lane < n ? ranked(c.v[lane]) : 0u, key2 = lane + 32 < n ? ranked(c.v[lane + 32]) : 0u;
+    int at = lane < n ? c.i[lane] : INT_MAX, at2 = lane + 32 < n ? c.i[lane + 32] : INT_MAX;
+    if (key2 > key || (key2 == key && at2 < at)) {
+        const uint32_t k = key;
+        const int i = at;
+        key = key2, at = at2, key2 = k, at2 = i;
+    }
     list_v = -INFINITY;
     for (int k = 0; k < top; ++k) {
         const uint32_t most = __reduce_max_sync(kAll, key);
         if (most <= kRankedNone) break;
-        const int win = __reduce_min_sync(kAll, key == most ? cand_i : INT_MAX);
-        if (key == most && cand_i == win) key = 0;
+        const int win = __reduce_min_sync(kAll, key == most ? at : INT_MAX);
+        if (key == most && at == win) key = key2, at = at2, key2 = 0u;
         if (lane == k) {
             list_v = from_ranked(most);
             list_i = win;
@@ -88,23 +100,20 @@ __device__ __forceinline__ void sort_candidates(float cand_v, int cand_i, int to
     }
 }
 
-struct Candidates {
-    float v[32];
-    int i[32];
-};
-
 // One warp's run z[0 .. n), n <= 32 NV, entries numbered from `first`.  The list
 // (list_v, list_i): lane k has the k-th largest entry above -inf found so far
 // (-inf: none), equal ones by number; entries of the run join it, all numbered
 // above those it came with.
 //
 // Alternatives: the `top`-th largest of the 32 lanes' maxima is a bound that the
-// `top` largest entries reach, and few others do; those that do are gathered, one
-// a lane, and sorted.  Where more than 32 do (many alternatives, ties) or fewer
-// than `top` lanes have an entry at all, they are taken out one by one instead.
-// (One by one throughout took 41 us on 4096 frames x 8 x 1026 with 5 alternatives,
-// twice as many instructions.)
-template <int NV>
+// `top` largest entries reach, and few others do (about 6 for 5, 130 for 32).
+// Halving the range between it and the maximum, at most a few times, gives one
+// that at least `top` and at most 64 reach; those are gathered and sorted.  Where
+// that fails (ties across the bound), with a NaN in the run, or where fewer than
+// `top` lanes have an entry above -inf, they are taken out one by one instead.
+// (One by one throughout took 41 us on 4096 frames x 8 x 1026 with 5 alternatives
+// and 158 us with 32; without alternatives the same frames take 22 us.)
+template <int NV, bool LISTED>  // LISTED: it comes with a list
 __device__ __forceinline__ Part warp_run(const float* z, int n, int first, float c, int top, Candidates& cand,
                                          float& list_v, int& list_i) {
     const int lane = threadIdx.x & 31;
@@ -158,48 +167,79 @@ __device__ __forceinline__ Part warp_run(const float* z, int n, int first, float
     }
     if (top == 0) return r;
 
-    const float old_v = list_v;
+    const float old_v = LISTED ? list_v : -INFINITY;
     const int old_i = list_i;
-    // the bound
-    float bound = -INFINITY;
+    // the bound, as a rank
+    uint32_t low = 0;
     {
         uint32_t key = ranked(fmaxf(m, old_v));
         for (int k = 0; k < top; ++k) {
-            const uint32_t most = __reduce_max_sync(kAll, key);
-            bound = most > kRankedNone ? from_ranked(most) : -INFINITY;
-            if (most <= kRankedNone) break;
-            if (lane == __ffs(__ballot_sync(kAll, key == most)) - 1) key = 0;
+            low = __reduce_max_sync(kAll, key);
+            if (low <= kRankedNone) break;
+            if (lane == __ffs(__ballot_sync(kAll, key == low)) - 1) key = 0;
         }
     }
-    int count = 33;
-    if (bound != -INFINITY) {
-        count = 0;
-        auto gather = [&](float x, int at) {
-            const unsigned in = __ballot_sync(kAll, x >= bound);
-            if (in) {
-                const int place = count + __popc(in & ((1u << lane) - 1));
-                if (x >= bound && place < 32) {
-                    cand.v[place] = x;
-                    cand.i[place] = at;
-                }
-                count += __popc(in);
+    if (low > kRankedNone && !r.nan) {
+        constexpr int kWords = (NV + 31) / 32;
+        unsigned marks[kWords];
+        float bound;
+        int count;
+        // an entry reaches the bound where (next value below it) - entry is negative:
+        // the sign bits, shifted in one by one
+        auto mark = [&](uint32_t rank) {
+            bound = from_ranked(rank);
+            // (the rank below +0 is -0's, which is as large: the one before it)
+            const float below = from_ranked(rank == 0x80000000u ? rank - 2 : rank - 1);
+            int mine = LISTED && old_v >= bound;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                marks[w] = 0;
+#pragma unroll
+                for (int i = 31; i >= 0; --i)
+                    if (32 * w + i < NV) marks[w] = __funnelshift_l(__float_as_uint(below - v[32 * w + i]), marks[w], 1);
+                mine += __popc(marks[w]);
             }
+            count = __reduce_add_sync(kAll, mine);
         };
-        gather(old_v, old_i);
-#pragma unroll
-        for (int j = 0; j < kChunks; ++j)
-            if (__any_sync(kAll, cm[j] >= bound)) {
-#pragma unroll
-                for (int i = 8 * j; i < 8 * j + 8 && i < NV; ++i) gather(v[i], first + 32 * i + lane);
+        mark(low);
+        uint32_t high = ranked(r.m) + 1u;  // reached by none of the run
+        if (LISTED) high = max(high, __reduce_max_sync(kAll, ranked(old_v)) + 1u);
+        while (count > 64 && low + 1u < high) {
+            const uint32_t mid = low + (high - low) / 2u;
+            mark(mid);
+            if (count >= top) {
+                low = mid;
+            } else {
+                high = mid;
+                count = 65;  // not yet
             }
-    }
-    if (count <= 32) {
-        __syncwarp();
-        const float cv = lane < count ? cand.v[lane] : -INFINITY;
-        const int ci = lane < count ? cand.i[lane] : INT_MAX;
-        __syncwarp();
-        sort_candidates(cv, ci, top, list_v, list_i);
-        return r;
+        }
+        if (count <= 64) {
+            // a lane gives out its marked entries, one a turn: most lanes have none, few
+            // have two
+            int place = 0;
+            auto gather = [&](bool in, float x, int at) {
+                const unsigned who = __ballot_sync(kAll, in);
+                if (in) {
+                    cand.v[place + __popc(who & ((1u << lane) - 1))] = x;
+                    cand.i[place + __popc(who & ((1u << lane) - 1))] = at;
+                }
+                place += __popc(who);
+            };
+            if (LISTED) gather(old_v >= bound, old_v, old_i);
+#pragma unroll
+            for (int w = 0; w < kWords; ++w)
+                while (__any_sync(kAll, marks[w] != 0)) {
+                    const bool in = marks[w] != 0;
+                    const int i = 32 * w + __ffs(marks[w]) - 1;
+                    gather(in, in ? z[lane + 32 * i] : 0.f, first + 32 * i + lane);
+                    marks[w] &= marks[w] - 1;
+                }
+            __syncwarp();
+            sort_candidates(cand, count, top, list_v, list_i);
+            __syncwarp();
+            return r;
+        }
     }
 
     float have = old_v;  // the old list's entry while it is not taken: chunk -1, the lowest numbers
@@ -323,7 +363,7 @@ __global__ void __launch_bounds__(kShortWarps * 32) logprobs_short_kernel(const 
     const float* z = row_of(p, item);
     float list_v = -INFINITY;
     int list_i = 0;
-    const Part r = warp_run<NV>(z, p.V, 0, kLog2e * p.inv_t, p.top, cand[threadIdx.x >> 5], list_v, list_i);
+    const Part r = warp_run<NV, false>(z, p.V, 0, kLog2e * p.inv_t, p.top, cand[threadIdx.x >> 5], list_v, list_i);
     finish(p, item, z, r, list_v, list_i);
 }
 
@@ -346,7 +386,7 @@ __global__ void __launch_bounds__(kLongWarps * 32) logprobs_long_kernel(const Lo
     float list_v = -INFINITY;
     int list_i = 0;
     for (int first = ((int)blockIdx.y * W + warp) * kRun; first < p.V; first += C * W * kRun)
-        r = join(r, warp_run<kRunNv>(z + first, min(kRun, p.V - first), first, c, p.top, lists[warp], list_v, list_i), c);
+        r = join(r, warp_run<kRunNv, true>(z + first, min(kRun, p.V - first), first, c, p.top, lists[warp], list_v, list_i), c);
     if (lane == 0) parts[warp] = r;
     lists[warp].v[lane] = list_v;
     lists[warp].i[lane] = list_i;

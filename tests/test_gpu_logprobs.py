@@ -74,6 +74,26 @@ def test_ties_go_to_the_lowest_code(ads, V):
     check(run(ads, z, codes_for(6, 2, V, 1), top), z, codes_for(6, 2, V, 1), top)
 
 
+@pytest.mark.parametrize("V", [300, 1026, 5000])
+@pytest.mark.parametrize("top", [1, 5, 20, 32])
+def test_alternatives_of_awkward_values(ads, V, top):
+    """Runs of equal values across the last alternative's, values one step apart,
+    zeros of both signs, subnormals, the largest and infinite ones."""
+    rng = np.random.default_rng(V + top)
+    z = synth.normal_f32(7, 4, (8, 2, V))
+    z[0] = rng.choice(np.float32([0.0, -0.0, 1e-45, -1e-45, 2e-45]), (2, V))
+    z[1] = np.float32(1) + rng.integers(0, 40, (2, V)).astype(np.float32) * np.float32(2 ** -23)
+    z[2, :, :200] = 3.0                             # far more than 64 at the maximum
+    z[3] = -rng.choice(np.float32([3.4028235e38, 3.4e38, 1.0]), (2, V))
+    z[4] = np.where(rng.random((2, V)) < 0.97, -np.inf, z[4])
+    z[5] = np.where(rng.random((2, V)) < 0.5, np.float32(-0.0), np.float32(-1))
+    z[5, 0, ::9] = 0.0
+    z[6] = np.round(z[6] * 30) / 30                 # ties everywhere
+    z[7] = np.sort(z[7])                            # all the largest at the end
+    codes = codes_for(8, 2, V, top)
+    check(run(ads, z, codes, top), z, codes, top)
+
+
 @pytest.mark.parametrize("V", [4, 1026, 40000])
 def test_masked_and_non_finite_rows(ads, V):
     z = synth.normal_f32(7, 9, (6, 1, V), std=2.5)
