@@ -232,6 +232,27 @@ __device__ __forceinline__ float quant_e4m3(float x) {
     return __half2float(*reinterpret_cast<__half*>(&h));
 }
 
+// 4-bit codes as operands of fp16 products.  Each 16-bit half of w holds two bytes of
+// two codes: nibble_bytes takes byte 0 of both halves (odd = 0) or byte 1 to the
+// low byte of a half under 0x64, which reads as the fp16 value 1024 + byte.
+// low_code and both_codes take the bias and the codes' centre away: u - 8 of the
+// low code u, and (u - 8) + 16 (u' - 8) of the byte, exact and normal fp16.  (Without the bias the codes are exact fp16 subnormals and
+// cost no subtraction, but the tensor core aligns products by their exponent
+// fields: sums then kept 18 bits, measured, not 23.)
+__device__ __forceinline__ uint32_t nibble_bytes(uint32_t w, int odd) {
+    return odd ? __byte_perm(w, 0x64646464u, 0x4341u) : (w & 0x00ff00ffu) | 0x64006400u;
+}
+__device__ __forceinline__ uint32_t minus_half2(uint32_t x, uint32_t bias) {
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&bias));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t low_code(uint32_t bytes, uint32_t bias = 0x64086408u) {
+    return minus_half2(bytes & 0xff0fff0fu, bias);
+}
+__device__ __forceinline__ uint32_t both_codes(uint32_t bytes, uint32_t bias = 0x64886488u) {
+    return minus_half2(bytes, bias);
+}
+
 // Pairs of fp32 in a 64-bit register: two lanes of arithmetic an instruction.
 typedef unsigned long long f32x2;
 __device__ __forceinline__ f32x2 pack2(float x, float y) {

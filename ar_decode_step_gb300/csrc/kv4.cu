@@ -291,17 +291,19 @@ __device__ __forceinline__ void norm_rope_exact(float4 x4, uint2 gb, const float
 // asynchronous copies, running maximum, sum and output, so nothing in the loop
 // waits for another warp.
 //
-// Both products run on the tensor cores (m16n8k16, fp16 operands, fp32 sums),
-// with the codes as they lie in memory: a nibble masked out of its 16-bit half
-// IS the fp16 subnormal u 2^-24, and a byte of two nibbles (u + 16 u') 2^-24,
-// exact, so a code costs about half an instruction and no conversion.  The
-// powers of two are taken back, and the even nibble out of the byte, on the
-// other operand or in the epilogue.
-//   scores  A = K codes (16 positions), B = queries.  score = sum over halves
-//           of s_K (q . u) + m_K sum(q): the scale and the minimum of a
-//           position enter in fp32 on the accumulators.
+// Both products run on the tensor cores (m16n8k16, fp16 operands, fp32 sums).
+// Codes enter centred, u - 8 and, from a whole byte, (u - 8) + 16 (u' - 8), exact
+// in fp16 (nibble_bytes and the next): one logical and one fp16 instruction per
+// two of them.  The even code is taken out of the byte on the other operand
+// (scores) or in the epilogue (output), and a half's minimum counts as
+// m + 8 s: with m and u the sums of values that cancel over the positions grew to
+// 200 times the result at 65536 positions, and its error to 1e-4 (2e-6 with V
+// codes all centred at 8, half a step off the middle).
+//   scores  A = K codes (16 positions), B = queries.  score = sum over halves of
+//           s_K q . (u - 8) + (m_K + 8 s_K) sum(q): a position's scale and
+//           centre enter in fp32 on the accumulators.
 //   output  A = V codes (16 channels of a half), B = p s_V of 16 positions;
-//           sum of p m_V beside it in fp32.
+//           sum of p (m_V + centre s_V) beside it in fp32.
 // The other operand is fp32 in two fp16 parts, of a value scaled by a power of
 // two towards fp16's upper end: 22 bits, and for small ones a floor of 2^-39
 // (queries) or 2^-33 (weights) of the largest, so nothing falls below fp32
@@ -359,10 +361,6 @@ __device__ __forceinline__ void split_h2(float x, float y, uint32_t* hi, uint32_
     *hi = *reinterpret_cast<const uint32_t*>(&h);
     *lo = *reinterpret_cast<const uint32_t*>(&r);
 }
-// Bytes 0 and 2 (s = 0) or 1 and 3 of w, each in the low byte of a 16-bit half.
-__device__ __forceinline__ uint32_t bytes(uint32_t w, int s) {
-    return s ? __byte_perm(w, 0u, 0x4341u) : w & 0x00ff00ffu;
-}
 // The transpose of an 8 x 8 matrix of 16-bit values held by a warp, lane
 // (row, pair of columns).
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
@@ -370,9 +368,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-// The biased exponent of w >= 0, at least 14, and the power of two that takes
+// The biased exponent of w >= 0, at least 15, and the power of two that takes
 // w to [2^14, 2^15).
-__device__ __forceinline__ int expo(float w) { return max((int)(__float_as_uint(w) >> 23), 14); }
+__device__ __forceinline__ int expo(float w) { return max((int)(__float_as_uint(w) >> 23), 15); }
 __device__ __forceinline__ float pow2_field(int field) { return __uint_as_float((uint32_t)field << 23); }
 __device__ __forceinline__ float to_2p15(int e) { return pow2_field(268 - e); }
 // For the weights, to [2^8, 2^9): six more doublings fit before fp16 ends, so
@@ -439,7 +437,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
     constexpr bool kPack = G <= 4;      // high and low parts in one product's columns
     constexpr int kParts = kPack ? 1 : 2;
     __shared__ uint2 frag[kParts][4][2][32];          // the scores' query operand, by lane
-    __shared__ float qhead[G][3];                     // sums over the halves, 2^24 over the operand's power of two
+    __shared__ float qhead[G][3];                     // sums over the halves, 1 over the operand's power of two
     __shared__ __align__(16) float vnew[kHeadDim];    // the new value row as cached
     __shared__ float wm[kAttnWarps + 1][G], wl[kAttnWarps + 1][G];
     __shared__ float merge_c[kMaxSplitUnits][G];      // a partial's weight in the merge
@@ -514,7 +512,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if ((lane & 15) == 0) qhead[warp][lane >> 4] = sum;
-        if (lane == 0) qhead[warp][2] = pow2_field(min(10 + e, 254));  // 2^24 / f
+        if (lane == 0) qhead[warp][2] = pow2_field(e - 14);  // 1 / f
         const int unit = (lane & 15) >> 1, w = (lane >> 4) + 2 * (unit & 1);
         __half* hi = reinterpret_cast<__half*>(&frag[0][w][0][4 * warp + (unit >> 1)]) + (lane & 1);
         __half* lo = reinterpret_cast<__half*>(&frag[kParts - 1][w][0][4 * (kPack ? warp + 4 : warp) + (unit >> 1)]) + (lane & 1);
@@ -596,7 +594,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
     // fv[h]: the power of two that keeps |weight x V scale| of half h under
     // 2^15; both per head.  l and omin are this lane's positions' shares.
     float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, fv[2][2], omin[2][2] = {};
-    fv[0][0] = fv[0][1] = fv[1][0] = fv[1][1] = to_2p9(14);
+    fv[0][0] = fv[0][1] = fv[1][0] = fv[1][1] = to_2p9(15);
     float o[2][4][4];  // [half][16-channel block][row r: heads, row r + 8: heads]
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -621,8 +619,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t u = bytes(w[0][i + h], s), v = bytes(w[1][i + h], s);
-                    const uint32_t a[4] = {u & 0x000f000fu, v & 0x000f000fu, u, v};
+                    const uint32_t u = nibble_bytes(w[0][i + h], s), v = nibble_bytes(w[1][i + h], s);
+                    const uint32_t a[4] = {low_code(u), low_code(v), both_codes(u), both_codes(v)};
                     if (i == 0 && s == 0)
                         mma16816_first(c[h], a, qb[0][i + h][s]);
                     else
@@ -630,15 +628,22 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
                     if (!kPack) mma16816(c[h], a, qb[kParts - 1][i + h][s]);
                 }
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 2; ++k) {
+            const float centre0 = fmaf(8.f, bf16lo(par[k].x), bf16hi(par[k].x));
+            const float centre1 = fmaf(8.f, bf16lo(par[k].y), bf16hi(par[k].y));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float x = fmaf(c[1][2 * k + j], bf16lo(par[k].y), c[0][2 * k + j] * bf16lo(par[k].x));
                 if (kPack) x += __shfl_xor_sync(0xffffffffu, x, 2);
-                sc[k][j] = fmaf(x, fq[j], fmaf(bf16hi(par[k].x), qsum[0][j], bf16hi(par[k].y) * qsum[1][j]));
+                sc[k][j] = fmaf(x, fq[j], fmaf(centre0, qsum[0][j], centre1 * qsum[1][j]));
             }
+        }
     };
     float wf[2][2][2];  // [half][position][head]
+    // V codes are centred at 8 at even positions (a register's low half) and at 7 at
+    // odd ones, 7.5 on average, the middle of a half's range
+    constexpr uint32_t kLowV = 0x64076408u, kBothV = 0x64776488u;
+    const float centre_v = r & 1 ? 7.f : 8.f;
     auto output = [&](int so) {
         uint2 vw[4];
 #pragma unroll
@@ -662,8 +667,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t sel = i < 2 ? 0x5410u : 0x7632u;
-                const uint32_t x = bytes(__byte_perm(w0, w1, sel), i & 1), y = bytes(__byte_perm(w2, w3, sel), i & 1);
-                const uint32_t a[4] = {x & 0x000f000fu, x, y & 0x000f000fu, y};
+                const uint32_t x = nibble_bytes(__byte_perm(w0, w1, sel), i & 1);
+                const uint32_t y = nibble_bytes(__byte_perm(w2, w3, sel), i & 1);
+                const uint32_t a[4] = {low_code(x, kLowV), both_codes(x, kBothV), low_code(y, kLowV), both_codes(y, kBothV)};
                 mma16816(o[h][i], a, b[0]);
                 if (!kPack) mma16816(o[h][i], a, b[kParts - 1]);
             }
@@ -708,7 +714,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
                     const int shrink = (int)(__float_as_uint(corr) >> 23) - 127;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int e_old = expo_of(fv[h][c]), e_new = max(e_old + shrink, 14);
+                        const int e_old = expo_of(fv[h][c]), e_new = max(e_old + shrink, 15);
                         const float k = corr * pow2_field(min(127 + e_old - e_new, 254));
                         fv[h][c] = to_2p9(e_new);
                         omin[h][c] *= corr;
@@ -736,7 +742,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t u = h ? par[k].y : par[k].x;
-                        omin[h][c] = fmaf(pw, bf16hi(u), omin[h][c]);
+                        omin[h][c] = fmaf(pw, fmaf(centre_v, bf16lo(u), bf16hi(u)), omin[h][c]);
                         vs[h][k][c] = pw * bf16lo(u);
                         wf[h][k][c] = vs[h][k][c] * fv[h][c];
                         wx = fmaxf(wx, fabsf(wf[h][k][c]));
@@ -793,13 +799,13 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
         float* po = reinterpret_cast<float*>(my_ring) + (hd + c) * kHeadDim + 8 * r;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float back = pow2_field(expo_of(fv[h][c]));  // 2^e, and 2^24 2^-8 = 2^16 below
+            const float back = pow2_field(expo_of(fv[h][c]) - 8);  // 1 / fv
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float x = i & 1 ? o[h][i >> 1][2 + c] - o[h][i >> 1][c] : o[h][i >> 1][c];
                 if (kPack) x += __shfl_xor_sync(0xffffffffu, x, 2);
-                v[i] = fmaf(x * (i & 1 ? 4096.f : 65536.f), back, omin[h][c]);
+                v[i] = fmaf(i & 1 ? x * 0.0625f : x, back, omin[h][c]);
             }
             if ((!kPack || t < 2) && hd + c < G) {
                 reinterpret_cast<float4*>(po + 64 * h)[0] = make_float4(v[0], v[1], v[2], v[3]);

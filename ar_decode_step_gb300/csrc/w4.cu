@@ -62,16 +62,15 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(const __nv_bfloat16* _
 // the weights once (at most 16 flops a byte), so everything else has to stay
 // below that: a weight may cost about 2.7 of an SM's lane instructions.
 //
-// Codes are the A operand of m16n8k16 products (fp16, fp32 sums) as they lie
-// in memory: a nibble masked out of its 16-bit half IS the fp16 subnormal
-// u 2^-24, and a byte of two nibbles is (u + 16 u') 2^-24, exact, so a code
-// costs half an instruction and no conversion; q u + q' u' = (q - q'/16) u +
-// (q'/16)(u + 16 u') moves the rest to the activations.  These are the B
-// operand: fp32, scaled per 128 group by a power of two to below 2^15 and split
-// into two fp16 parts (22 bits, and 2^-39 of the group's largest).  Up to four
-// vectors take columns 2m and 2m + 1 of one product, eight a product for each
+// Codes are the A operand of m16n8k16 products (fp16, fp32 sums), centred: u - 8
+// and, from a whole byte, (u - 8) + 16 (u' - 8), exact in fp16, one logical and one
+// fp16 instruction per two of them; a (u - 8) + a' (u' - 8) = (a - a'/16)(u - 8) +
+// (a'/16)((u - 8) + 16 (u' - 8)) moves the rest to the activations.  These are
+// the B operand: fp32, scaled per 128 group by a power of two to below 2^15 and
+// split into two fp16 parts (22 bits, and 2^-39 of the group's largest).  Up to
+// four vectors take columns 2m and 2m + 1 of one product, eight a product for each
 // part.  Group sums leave the tensor core once a group and are scaled and added
-// in fp32: acc += s (2^(24-e) part - 8 sum(a)).
+// in fp32.
 //
 // About one block an SM.  A block takes tiles of 16 rows (epi 2: a gate and an up
 // tile) of all of K, or of a share of K where its activations or its tiles would
@@ -101,13 +100,9 @@ __device__ __forceinline__ void mma16816_f16(float c[4], uint32_t a0, uint32_t a
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Bytes 0 and 2 or 1 and 3 of w, each in the low byte of a 16-bit half.
-__device__ __forceinline__ uint32_t even_bytes(uint32_t w) { return w & 0x00ff00ffu; }
-__device__ __forceinline__ uint32_t odd_bytes(uint32_t w) { return __byte_perm(w, 0u, 0x4341u); }
-
 // Shared memory of a block: [rows: tiles x parts x 16][activations: share x 4 words
-// x columns x 4 pieces x 16 bytes][per group and vector: (2^24 over its power of
-// two, 8 sum)][scales: tiles x parts x share x 16 bf16][sums: outputs x parts x
+// x columns x 4 pieces x 16 bytes][per group and vector: 1 over its power of
+// two][scales: tiles x parts x share x 16 bf16][sums: outputs x parts x
 // warps][sums of squares: MV x warps][totals of the block: outputs x parts, MV].
 __host__ __device__ constexpr int columns_of(int mv) { return 2 * mv; }
 __host__ __device__ constexpr int act_group_bytes(int mv) { return 4 * columns_of(mv) * 64; }
@@ -121,7 +116,7 @@ __host__ __device__ inline W4Smem smem_of(int mv, int parts, int tiles, int shar
     const uint32_t outs = tiles * 16 * mv * parts;
     o.act = tiles * parts * 16 * row_pitch(share);
     o.par = o.act + share * act_group_bytes(mv);
-    o.scales = o.par + share * mv * 8;
+    o.scales = o.par + share * mv * 4;
     o.sums = o.scales + tiles * parts * share * 32;
     o.sq = o.sums + outs * warps * 4;
     o.tot = o.sq + mv * warps * 4;
@@ -222,7 +217,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
     }
 
     // ---- this warp's slice of the activations
-    float2* act_par = reinterpret_cast<float2*>(smem + o.par);
+    float* act_par = reinterpret_cast<float*>(smem + o.par);
     float* sq = reinterpret_cast<float*>(smem + o.sq);  // [W][MV]
     float ss[MV];
 #pragma unroll
@@ -249,14 +244,13 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
                        (lane >> 3) * 16 + (lane & 1) * 8;
 #pragma unroll
         for (int m = 0; m < MV; ++m) {
-            const float sum = warp_sum((a[m][0] + a[m][1]) + (a[m][2] + a[m][3]));
             const uint32_t amax = __reduce_max_sync(
                 0xffffffffu,
                 __float_as_uint(fmaxf(fmaxf(fabsf(a[m][0]), fabsf(a[m][1])), fmaxf(fabsf(a[m][2]), fabsf(a[m][3])))));
             // the group's power of two: largest to [2^14, 2^15)
-            const int e = max((int)(amax >> 23), 14);
+            const int e = max((int)(amax >> 23), 15);
             const float f = __uint_as_float((uint32_t)(268 - e) << 23);
-            if (lane == 0) act_par[g * MV + m] = make_float2(__uint_as_float((uint32_t)min(10 + e, 254) << 23), 8.f * sum);
+            if (lane == 0) act_par[g * MV + m] = __uint_as_float((uint32_t)(e - 14) << 23);  // 1 / f
             // channels 4 l .. 4 l + 3 are nibbles 4 (l % 2) + 0..3 of word (l / 2) % 4 of
             // piece l / 8: of the pairs (0, 4), (1, 5), (2, 6), (3, 7) an even lane
             // has the low halves, an odd lane the high ones
@@ -300,7 +294,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
             b[0][w] = column ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
             if (MV == 8) b[kVecs - 1][w] = *reinterpret_cast<const uint4*>(at + 512);
         }
-        float2 ap[kVecs];
+        float ap[kVecs];
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) ap[v] = act_par[g * MV + min(kVecs * t + v, MV - 1)];
         const uint8_t* row = smem + r * pitch + t * 16 + g * 64;
@@ -317,25 +311,27 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
             float d[2][4] = {};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-                const uint32_t x0 = even_bytes(ua[w]), y0 = even_bytes(ub[w]), x1 = odd_bytes(ua[w]), y1 = odd_bytes(ub[w]);
-                const uint32_t xl0 = x0 & 0x000f000fu, yl0 = y0 & 0x000f000fu, xl1 = x1 & 0x000f000fu, yl1 = y1 & 0x000f000fu;
+                const uint32_t x0 = nibble_bytes(ua[w], 0), y0 = nibble_bytes(ub[w], 0);
+                const uint32_t x1 = nibble_bytes(ua[w], 1), y1 = nibble_bytes(ub[w], 1);
+                const uint32_t xl0 = low_code(x0), yl0 = low_code(y0), xl1 = low_code(x1), yl1 = low_code(y1);
+                const uint32_t xb0 = both_codes(x0), yb0 = both_codes(y0), xb1 = both_codes(x1), yb1 = both_codes(y1);
 #pragma unroll
                 for (int v = 0; v < kVecs; ++v) {
-                    mma16816_f16(d[0], xl0, yl0, x0, y0, b[v][w].x, b[v][w].y);
-                    mma16816_f16(d[1], xl1, yl1, x1, y1, b[v][w].z, b[v][w].w);
+                    mma16816_f16(d[0], xl0, yl0, xb0, yb0, b[v][w].x, b[v][w].y);
+                    mma16816_f16(d[1], xl1, yl1, xb1, yb1, b[v][w].z, b[v][w].w);
                 }
             }
             if (MV == 8) {
 #pragma unroll
                 for (int v = 0; v < kVecs; ++v) {
-                    const float ya = sa * fmaf(d[0][v] + d[1][v], ap[v].x, -ap[v].y);
-                    const float yb = sb * fmaf(d[0][2 + v] + d[1][2 + v], ap[v].x, -ap[v].y);
+                    const float ya = sa * (ap[v] * (d[0][v] + d[1][v]));
+                    const float yb = sb * (ap[v] * (d[0][2 + v] + d[1][2 + v]));
                     out[v] = g == g0 ? ya : out[v] + ya;
                     out[8 * MV + v] = g == g0 ? yb : out[8 * MV + v] + yb;
                 }
             } else if (t < MV) {
-                const float ya = sa * fmaf((d[0][0] + d[1][0]) + (d[0][1] + d[1][1]), ap[0].x, -ap[0].y);
-                const float yb = sb * fmaf((d[0][2] + d[1][2]) + (d[0][3] + d[1][3]), ap[0].x, -ap[0].y);
+                const float ya = sa * (ap[0] * ((d[0][0] + d[1][0]) + (d[0][1] + d[1][1])));
+                const float yb = sb * (ap[0] * ((d[0][2] + d[1][2]) + (d[0][3] + d[1][3])));
                 out[0] = g == g0 ? ya : out[0] + ya;
                 out[8 * MV] = g == g0 ? yb : out[8 * MV] + yb;
             }
