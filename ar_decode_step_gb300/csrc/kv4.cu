@@ -316,7 +316,7 @@ __device__ __forceinline__ void norm_rope_exact(float4 x4, uint2 gb, const float
 // sums instead of 48, so 12 warps an SM instead of 16.)
 constexpr int kAttnWarps = 16;
 constexpr int kTilePos = 16;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kStageV = kTilePos * kRowBytes;             // K rows, then V rows (permuted)
 constexpr int kStagePar = 2 * kStageV;                    // then K and V parameters
 constexpr int kStageBytes = kStagePar + 2 * kTilePos * 8;
@@ -444,7 +444,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
     __shared__ float merge_l[G];
     __shared__ int s_last;
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // the warp's number by a shuffle: the compiler then keeps the loop's control in
+    // uniform registers
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int r = lane >> 2, t = lane & 3;
     const int g = blockIdx.x / p.S, split = blockIdx.x % p.S;
     const bool has_new = split == p.S - 1;
@@ -958,6 +960,10 @@ cudaError_t launch_attn_kv4(const Kv4Params& p, cudaStream_t s) {
     return launch_ordered(attn_kv4_kernel<G>, dim3(p.n_kv * p.S), dim3(kAttnWarps * 32), kAttnSmem, s, 1, 1, p);
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 int report_kv4(cudaError_t e, const char* what) {
@@ -989,6 +995,11 @@ int rows_ok(const void* k, const void* v, const void* k4, const void* v4, const 
         return TTS_ERR_ARG;
     if (p1 > max_pos) return TTS_ERR_FULL;
     if (p1 > stride) return TTS_ERR_ARG;
+    const size_t rows = (size_t)n_kv * max_pos, bytes = (size_t)n_kv * stride * kHeadDim * 2;
+    for (const void* side : {k, v})
+        if (overlap(side, bytes, k4, rows * kRowBytes) || overlap(side, bytes, v4, rows * kRowBytes) ||
+            overlap(side, bytes, kp, rows * 8) || overlap(side, bytes, vp, rows * 8))
+            return TTS_ERR_ARG;
     return TTS_OK;
 }
 
@@ -1043,6 +1054,23 @@ extern "C" int tts_attention_decode_kv4(const float* qkv, const void* q_norm, co
         misaligned(kv_row, 16) || misaligned(workspace, 16))
         return TTS_ERR_ARG;
     if (workspace_bytes < workspace_bytes_for(n_q, n_kv)) return TTS_ERR_ARG;
+    // what one block writes while others still read
+    {
+        const size_t head = sizeof(float) * kHeadDim, rows = (size_t)n_kv * max_pos;
+        const struct {
+            const void* p;
+            size_t n;
+        } made[] = {{out, n_q * head}, {kv_row, kv_row ? 2 * n_kv * head : 0}, {k4, rows * kRowBytes}, {v4, rows * kRowBytes},
+                    {k_par, rows * 8}, {v_par, rows * 8}, {workspace, workspace_bytes_for(n_q, n_kv)}},
+          read[] = {{qkv, (n_q + 2 * n_kv) * head}, {q_norm, 2 * kHeadDim}, {k_norm, 2 * kHeadDim}};
+        for (size_t i = 0; i < sizeof(made) / sizeof(made[0]); ++i) {
+            if (!made[i].p) continue;
+            for (const auto& r : read)
+                if (overlap(made[i].p, made[i].n, r.p, r.n)) return TTS_ERR_ARG;
+            for (size_t j = 0; j < i; ++j)
+                if (made[j].p && overlap(made[i].p, made[i].n, made[j].p, made[j].n)) return TTS_ERR_ARG;
+        }
+    }
     if (pos >= max_pos) return TTS_ERR_FULL;
     Kv4Params p{};
     p.qkv = qkv;

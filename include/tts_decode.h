@@ -401,7 +401,7 @@ int tts_quantize_w4_weight(const void* W, int N, int K, void* W4, void* s, void*
  *   epi 0: y = a . W^T; epi 1: y = resid + a . W^T; epi 2: SwiGLU,
  *   y = silu(a . gate^T) * (a . up^T).  y: DEVICE fp32 [M][N]; resid: DEVICE
  *   fp32 [M][N] for epi 1 (may be y itself), NULL otherwise.
- * Activations stay fp32 (no rounding to 16 bits), sums are fp32, and every
+ * Activations stay fp32 (as two fp16 parts, 22 bits), sums are fp32, and every
  * result is deterministic.  1 <= M <= 8, K % 128 == 0, 128 <= K <= 12288, any
  * N from 1 to 2^24.  x, W4 and gamma 16-byte, s 4-byte aligned; y overlaps no input
  * (but resid == y).  Enqueued on `stream` (NULL: the default stream); does
@@ -428,7 +428,8 @@ int tts_gemv_w4(const float* x, const void* W4, const void* s, const float* resi
  * n_kv up to 1024.
  * Enqueued on `stream` (NULL: the default stream); neither synchronises.
  * TTS_ERR_FULL if p1 > max_pos; TTS_ERR_ARG if p1 exceeds the bf16 cache's
- * stride, for bad sizes, NULL or misaligned pointers. */
+ * stride, for bad sizes, NULL or misaligned pointers, or where a bf16 cache
+ * overlaps the 4-bit one. */
 int tts_quantize_kv4(const void* k, const void* v, int n_kv, int p0, int p1, int src_stride, void* k4, void* v4,
                      void* k_par, void* v_par, int max_pos, void* stream);
 int tts_dequantize_kv4(const void* k4, const void* v4, const void* k_par, const void* v_par, int n_kv, int p0, int p1,
@@ -452,7 +453,8 @@ int tts_dequantize_kv4(const void* k4, const void* v4, const void* k_par, const 
  * stream share one, of any shapes.  Enqueued on `stream` (NULL: the default stream); does not
  * synchronise; may be captured (a replay repeats position pos).
  * TTS_ERR_FULL if pos >= max_pos; TTS_ERR_ARG for bad sizes, a short
- * workspace, NULL or misaligned (16 bytes) pointers. */
+ * workspace, NULL or misaligned (16 bytes) pointers, or where anything that is
+ * written overlaps another argument. */
 int tts_attention_kv4_workspace(int n_q, int n_kv, size_t* bytes);
 int tts_attention_decode_kv4(const float* qkv, const void* q_norm, const void* k_norm, void* k4, void* v4, void* k_par,
                              void* v_par, float* out, float* kv_row, int n_q, int n_kv, int max_pos, int pos,

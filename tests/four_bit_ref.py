@@ -44,10 +44,10 @@ def gemv_w4(x, b, s_bits, epi=0, resid=None, gamma_bits=None, eps=1e-6):
     Each product a w of the kernel is exact up to the split of a into two fp16
     terms (4 U a); a group's 128 products are added in at most 8 steps of 2^-22
     of the group's magnitude, and the groups' results and the partial sums of
-    up to 32 warps in one fp32 add each.  The nibbles are used as 0..15 and
-    8 sum(a) is subtracted, so magnitudes count 16 |a| s per product, halved
-    here because a nibble's weight averages out only in the value, not the
-    bound: B = sum |a| 16 s.  The normalisation adds 16 U."""
+    up to 32 warps in one fp32 add each.  A byte's two codes are one operand, at
+    most 8 + 16 . 8 times a 16th of an activation, beside 8 times the other, so
+    magnitudes count 8 (1 + 1 / 8) |a| s per product and code, below B = sum |a|
+    9 s.  The normalisation adds 16 U."""
     x = np.asarray(x, np.float64)
     w = dequant_w4(b, s_bits)
     K = x.shape[1]
@@ -55,7 +55,7 @@ def gemv_w4(x, b, s_bits, epi=0, resid=None, gamma_bits=None, eps=1e-6):
     if gamma_bits is not None:
         a = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * bf16_val(gamma_bits)
     acc = a @ w.T
-    B = 16 * np.abs(a) @ np.repeat(bf16_val(s_bits), 128, axis=1).T
+    B = 9 * np.abs(a) @ np.repeat(bf16_val(s_bits), 128, axis=1).T
     tol = B * U * (4 + 8 * 4 + K / 128 + 32 + 16)
     if epi == 1:
         y = np.asarray(resid, np.float64) + acc
@@ -97,9 +97,11 @@ def dequant_kv4(b, par_bits):
 
 
 def kv4_size(b, par_bits):
-    """|minimum| + 15 scale per channel: what a cached value's rounding scales with."""
-    p = np.abs(bf16_val(par_bits))
-    return np.repeat(p[..., 1] + 15 * p[..., 0], 64, axis=-1)
+    """|middle of the range| + 8.5 scale per channel: what the terms of a sum over a
+    cached value scale with, its code taken from the middle (at most 8 steps off
+    it, and half a step where the middle is between two codes)."""
+    p = bf16_val(par_bits)
+    return np.repeat(np.abs(p[..., 1] + 7.5 * p[..., 0]) + 8.5 * np.abs(p[..., 0]), 64, axis=-1)
 
 
 def norm_rope(x, gain_bits, pos, eps, theta):
@@ -114,13 +116,13 @@ def attention_kv4(qkv, qn_bits, kn_bits, k4, kp, v4, vp, n_q, n_kv, pos, eps=1e-
     """The cache arrays (bytes and parameter bits, [n_kv][max_pos]...) with row
     pos written, and the output with its tolerance: (k4, kp, v4, vp, out, tol).
 
-    A score is off by S = sum |q| (|minimum| + 15 scale) / sqrt(128) times the
+    A score is off by S = sum |q| kv4_size / sqrt(128) times the
     relative error of the query (norm, rotation and its split: 16 U), of the
     dot product (8 steps of 4 U and the half's terms: 48 U) and of the
     exponential's argument; a probability by twice the largest such error plus
     the exponential's own 8 U; the output by that and the sums over the
     positions (at most 64 + n / 512 adds to any value beyond 512 positions a
-    warp), each of sum p (|minimum| + 15 scale)."""
+    warp), each of sum p kv4_size."""
     x = np.asarray(qkv, np.float64).reshape(-1, D)
     q = norm_rope(x[:n_q], qn_bits, pos, eps, theta)
     kb = bf16_bits(norm_rope(x[n_q:n_q + n_kv], kn_bits, pos, eps, theta).astype(np.float32))

@@ -58,6 +58,8 @@ def test_quantize_kv4_refusals(lib):
     bad += [dict({n: KV[n] + 8}) for n in ("k", "v", "k4", "v4", "k_par", "v_par")]
     bad += [dict(n_kv=0), dict(p0=-1), dict(p0=9), dict(stride=7), dict(max_pos=0), dict(max_pos=(1 << 20) + 1)]
     refuse(lib.tts_quantize_kv4, KV, bad)
+    bad += [dict(k=A[2]), dict(v=A[2] + 2 * 16 * 64 - 16), dict(k4=A[1] + 2 * 16 * 256 - 16), dict(v_par=A[0] + 64)]
+    refuse(lib.tts_quantize_kv4, KV, bad)
     refuse(lib.tts_quantize_kv4, KV, [dict(p1=17), dict(max_pos=7)], FULL)
     assert lib.tts_quantize_kv4(*dict(KV, p0=5, p1=5).values()) == 0  # nothing to do
 
@@ -83,6 +85,12 @@ def test_attention_kv4_refusals(lib):
     bad += [dict(n_q=24), dict(n_q=8, n_kv=3), dict(n_q=0), dict(n_kv=0), dict(n_q=128), dict(n_q=8192, n_kv=8192),
             dict(max_pos=0), dict(max_pos=(1 << 20) + 1), dict(pos=-1), dict(eps=-1e-6), dict(theta=0.0),
             dict(theta=float("inf")), dict(theta=float("nan")), dict(ws_bytes=n - 1), dict(ws_bytes=0)]
+    refuse(lib.tts_attention_decode_kv4, good, bad)
+    # written over something that another block reads, or twice
+    row = 128 * 4
+    bad += [dict(out=A[0]), dict(out=A[0] + 48 * row - 16), dict(kv_row=A[0] + 16), dict(kv_row=A[7]),
+            dict(out=A[3] + 8 * 64 * 64 - 16), dict(v4=A[3]), dict(v_par=A[5] + 16), dict(ws=A[7] + 32 * row - 16),
+            dict(out=A[8] + n - 16), dict(out=A[2])]
     refuse(lib.tts_attention_decode_kv4, good, bad)
     refuse(lib.tts_attention_decode_kv4, good, [dict(pos=64), dict(pos=1 << 20)], FULL)
 

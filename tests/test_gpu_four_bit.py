@@ -247,6 +247,24 @@ def test_attention_kv4_long(ads):
     a.check()
 
 
+@pytest.mark.parametrize("pos", [40, 3000, 60000])
+def test_attention_kv4_is_as_exact_as_fp32_on_the_values(ads, pos):
+    """The 2-norm of the error stays within that of the formula evaluated in fp32 on
+    the dequantised cache (numpy, which adds pairwise), also where the values of
+    many positions cancel to a small result."""
+    a = Attn(ads, 4, 1, pos + 1, pos)
+    a.call()
+    k4, kp, v4, vp, want, _ = ref.attention_kv4(a.qkv, a.qn, a.kn, a.k4, a.kp, a.v4, a.vp, 4, 1, pos)
+    q = ref.norm_rope(a.qkv.astype(np.float64).reshape(-1, D)[:4], a.qn, pos, 1e-6, 1e6).astype(np.float32)
+    k = ref.dequant_kv4(k4[0], kp[0]).astype(np.float32)
+    v = ref.dequant_kv4(v4[0], vp[0]).astype(np.float32)
+    z = q @ k.T / np.float32(np.sqrt(D))
+    p = np.exp(z - z.max(-1, keepdims=True))
+    plain = (p[:, :, None] * v[None]).sum(1) / p.sum(-1, keepdims=True)
+    err = lambda x: np.linalg.norm(x.astype(np.float64).ravel() - want) / np.linalg.norm(want)
+    assert err(host(a.out)) <= 2 * err(plain) + ref.U
+
+
 def test_attention_kv4_far_offsets(ads):
     """Heads whose rows lie past 2^32 bytes: only the rows read are filled."""
     import torch
