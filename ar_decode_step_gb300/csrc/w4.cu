@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdio>
 #include <mutex>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 
@@ -100,13 +101,21 @@ __device__ __forceinline__ void mma16816_f16(float c[4], uint32_t a0, uint32_t a
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// d = A B, without clearing d first
+__device__ __forceinline__ void mma16816_f16_first(float c[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                                   uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // Shared memory of a block: [rows: tiles x parts x 16][activations: share x 4 words
 // x columns x 4 pieces x 16 bytes][per group and vector: 1 over its power of
 // two][scales: tiles x parts x share x 16 bf16][sums: outputs x parts x
 // warps][sums of squares: MV x warps][totals of the block: outputs x parts, MV].
 __host__ __device__ constexpr int columns_of(int mv) { return 2 * mv; }
 __host__ __device__ constexpr int act_group_bytes(int mv) { return 4 * columns_of(mv) * 64; }
-__host__ __device__ constexpr int max_warps(int mv) { return mv >= 4 ? 16 : 24; }
+__host__ __device__ constexpr int max_warps(int mv) { return mv >= 4 ? 16 : 20; }
 __host__ __device__ inline int row_pitch(int share) { return share * 64 + (share & 1 ? 0 : 64); }
 struct W4Smem {
     uint32_t act, par, scales, sums, sq, tot, total;
@@ -130,7 +139,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
     __shared__ __align__(8) uint64_t bars[kMaxTiles * PARTS];
     __shared__ int late;  // a tile did not arrive: the outputs are NaN
     constexpr int kVecs = MV == 8 ? 2 : 1;  // vectors a lane adds up
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = c.warps;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), W = c.warps;
     const int r = lane >> 2, t = lane & 3;
     const int groups = p.K / kW4Group, rank = blockIdx.z, split = 1 << c.log_split;
     const int k0 = groups * rank >> c.log_split, kg = (groups * (rank + 1) >> c.log_split) - k0;  // this block's groups of K
@@ -300,43 +309,71 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
         const uint8_t* row = smem + r * pitch + t * 16 + g * 64;
         const __nv_bfloat16* sc = scl + g * 16 + r;
         float* out = sums + r * MV + kVecs * t;
-        for (int q = 0; q < nt * PARTS; ++q) {
-            if (g == g0 && !mbar_wait(&bars[q], 0)) late = 1;
-            const uint4 wa = *reinterpret_cast<const uint4*>(row);
-            const uint4 wb = *reinterpret_cast<const uint4*>(row + 8 * pitch);
-            const float sa = __bfloat162float(sc[0]), sb = __bfloat162float(sc[8]);
-            row += 16 * pitch;
-            sc += 16 * c.share;
-            const uint32_t ua[4] = {wa.x, wa.y, wa.z, wa.w}, ub[4] = {wb.x, wb.y, wb.z, wb.w};
-            float d[2][4] = {};
+        // n tiles at a time: their loads, conversions and products are independent
+        auto tiles = [&](int q, auto n_) {
+            constexpr int n = decltype(n_)::value;
+            if (g == g0) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint32_t x0 = nibble_bytes(ua[w], 0), y0 = nibble_bytes(ub[w], 0);
-                const uint32_t x1 = nibble_bytes(ua[w], 1), y1 = nibble_bytes(ub[w], 1);
-                const uint32_t xl0 = low_code(x0), yl0 = low_code(y0), xl1 = low_code(x1), yl1 = low_code(y1);
-                const uint32_t xb0 = both_codes(x0), yb0 = both_codes(y0), xb1 = both_codes(x1), yb1 = both_codes(y1);
-#pragma unroll
-                for (int v = 0; v < kVecs; ++v) {
-                    mma16816_f16(d[0], xl0, yl0, xb0, yb0, b[v][w].x, b[v][w].y);
-                    mma16816_f16(d[1], xl1, yl1, xb1, yb1, b[v][w].z, b[v][w].w);
-                }
+                for (int k = 0; k < n; ++k)
+                    if (!mbar_wait(&bars[q + k], 0)) late = 1;
             }
-            if (MV == 8) {
+            uint4 wa[n], wb[n];
+            float sa[n], sb[n], d[n][2][4];
 #pragma unroll
-                for (int v = 0; v < kVecs; ++v) {
-                    const float ya = sa * (ap[v] * (d[0][v] + d[1][v]));
-                    const float yb = sb * (ap[v] * (d[0][2 + v] + d[1][2 + v]));
-                    out[v] = g == g0 ? ya : out[v] + ya;
-                    out[8 * MV + v] = g == g0 ? yb : out[8 * MV + v] + yb;
-                }
-            } else if (t < MV) {
-                const float ya = sa * (ap[0] * ((d[0][0] + d[1][0]) + (d[0][1] + d[1][1])));
-                const float yb = sb * (ap[0] * ((d[0][2] + d[1][2]) + (d[0][3] + d[1][3])));
-                out[0] = g == g0 ? ya : out[0] + ya;
-                out[8 * MV] = g == g0 ? yb : out[8 * MV] + yb;
+            for (int k = 0; k < n; ++k) {
+                wa[k] = *reinterpret_cast<const uint4*>(row + k * 16 * pitch);
+                wb[k] = *reinterpret_cast<const uint4*>(row + (k * 16 + 8) * pitch);
+                sa[k] = __bfloat162float(sc[k * 16 * c.share]);
+                sb[k] = __bfloat162float(sc[k * 16 * c.share + 8]);
             }
-            out += 16 * MV;
-        }
+            row += n * 16 * pitch;
+            sc += n * 16 * c.share;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+                for (int k = 0; k < n; ++k) {
+                    const uint32_t ua = w == 0 ? wa[k].x : w == 1 ? wa[k].y : w == 2 ? wa[k].z : wa[k].w;
+                    const uint32_t ub = w == 0 ? wb[k].x : w == 1 ? wb[k].y : w == 2 ? wb[k].z : wb[k].w;
+#pragma unroll
+                    for (int odd = 0; odd < 2; ++odd) {
+                        const uint32_t x = nibble_bytes(ua, odd), y = nibble_bytes(ub, odd);
+                        const uint32_t xl = low_code(x), yl = low_code(y), xb = both_codes(x), yb = both_codes(y);
+#pragma unroll
+                        for (int v = 0; v < kVecs; ++v) {
+                            const uint32_t b0 = odd ? b[v][w].z : b[v][w].x, b1 = odd ? b[v][w].w : b[v][w].y;
+                            if (w == 0 && v == 0)
+                                mma16816_f16_first(d[k][odd], xl, yl, xb, yb, b0, b1);
+                            else
+                                mma16816_f16(d[k][odd], xl, yl, xb, yb, b0, b1);
+                        }
+                    }
+                }
+#pragma unroll
+            for (int k = 0; k < n; ++k) {
+                float y[2][kVecs];
+#pragma unroll
+                for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float x;
+                        if (MV == 8)
+                            x = d[k][0][2 * h + v] + d[k][1][2 * h + v];
+                        else
+                            x = (d[k][0][2 * h] + d[k][1][2 * h]) + (d[k][0][2 * h + 1] + d[k][1][2 * h + 1]);
+                        y[h][v] = (h ? sb[k] : sa[k]) * (ap[v] * x);
+                    }
+                if (MV == 8 || t < MV) {
+#pragma unroll
+                    for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) out[h * 8 * MV + v] = g == g0 ? y[h][v] : out[h * 8 * MV + v] + y[h][v];
+                }
+                out += 16 * MV;
+            }
+        };
+        int q = 0;
+        for (; q + 2 <= nt * PARTS; q += 2) tiles(q, std::integral_constant<int, 2>{});
+        if (q < nt * PARTS) tiles(q, std::integral_constant<int, 1>{});
     }
     if (g0 == g1)  // no group: nothing of this warp's, but its copies
         for (int i = lane; i < outs * PARTS; i += 32) sums[i] = 0.f;
