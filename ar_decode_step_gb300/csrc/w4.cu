@@ -115,6 +115,11 @@ __device__ __forceinline__ void mma16816_f16_first(float c[4], uint32_t a0, uint
 // warps][sums of squares: MV x warps][totals of the block: outputs x parts, MV].
 __host__ __device__ constexpr int columns_of(int mv) { return 2 * mv; }
 __host__ __device__ constexpr int act_group_bytes(int mv) { return 4 * columns_of(mv) * 64; }
+// Whether a warp's sums take the place of its first group's activations, which are
+// in registers by then.  It brings gate/up of four vectors at 2560 x 9728 to one
+// block an SM (12.7 us against 17.9); elsewhere room is left or nothing is gained,
+// and a place of their own is 2 to 9 % faster.
+__host__ __device__ constexpr bool sums_in_act(int mv, int parts) { return mv == 4 && parts == 2; }
 __host__ __device__ constexpr int max_warps(int mv) { return mv >= 4 ? 16 : 20; }
 __host__ __device__ inline int row_pitch(int share) { return share * 64 + (share & 1 ? 0 : 64); }
 struct W4Smem {
@@ -127,7 +132,7 @@ __host__ __device__ inline W4Smem smem_of(int mv, int parts, int tiles, int shar
     o.par = o.act + share * act_group_bytes(mv);
     o.scales = o.par + share * mv * 4;
     o.sums = o.scales + tiles * parts * share * 32;
-    o.sq = o.sums + outs * warps * 4;
+    o.sq = o.sums + (sums_in_act(mv, parts) ? 0 : outs * warps * 4);
     o.tot = o.sq + mv * warps * 4;
     o.total = o.tot + (outs + mv) * 4;
     return o;
@@ -293,7 +298,10 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
     __syncthreads();  // the scales come from other warps
 
     // ---- the products: a group's activations in registers, all tiles past them
-    float* sums = reinterpret_cast<float*>(smem + o.sums) + (size_t)warp * outs * PARTS;  // [W][tile x parts][row][vector]
+    constexpr bool kInAct = sums_in_act(MV, PARTS);
+    static_assert(!kInAct || kMaxTiles / 2 * 16 * MV * PARTS * 4 <= act_group_bytes(MV), "a warp's sums fit a group");
+    float* sums = kInAct ? reinterpret_cast<float*>(smem + o.act + g0 * act_group_bytes(MV))
+                         : reinterpret_cast<float*>(smem + o.sums) + (size_t)warp * outs * PARTS;  // [tile x parts][row][vector]
     const bool column = MV == 8 || r < 2 * MV;
     for (int g = g0; g < g1; ++g) {
         uint4 b[kVecs][4];
@@ -306,6 +314,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
         float ap[kVecs];
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) ap[v] = act_par[g * MV + min(kVecs * t + v, MV - 1)];
+        if (kInAct && g == g0) __syncwarp();  // all lanes have read what the sums replace
         const uint8_t* row = smem + r * pitch + t * 16 + g * 64;
         const __nv_bfloat16* sc = scl + g * 16 + r;
         float* out = sums + r * MV + kVecs * t;
@@ -375,7 +384,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
         for (; q + 2 <= nt * PARTS; q += 2) tiles(q, std::integral_constant<int, 2>{});
         if (q < nt * PARTS) tiles(q, std::integral_constant<int, 1>{});
     }
-    if (g0 == g1)  // no group: nothing of this warp's, but its copies
+    if (!kInAct && g0 == g1)  // no group: nothing of this warp's, but its copies
         for (int i = lane; i < outs * PARTS; i += 32) sums[i] = 0.f;
     for (int q = 0; q < nt * PARTS; ++q)
         if (g0 == g1 && !mbar_wait(&bars[q], 0)) late = 1;
@@ -396,7 +405,14 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
 #pragma unroll 4
         for (int w = 0; w < W; ++w) {
 #pragma unroll
-            for (int h = 0; h < PARTS; ++h) v[h] += all[(size_t)w * outs * PARTS + first + h * 16 * MV];
+            for (int h = 0; h < PARTS; ++h)
+                if (!kInAct) {
+                    v[h] += all[(size_t)w * outs * PARTS + first + h * 16 * MV];
+                } else {  // where warp w's first group was, if it had any
+                    const int from = (int)(kg * w * c.magic >> 32), to = (int)(kg * (w + 1) * c.magic >> 32);
+                    const float* theirs = reinterpret_cast<const float*>(smem + o.act + from * act_group_bytes(MV));
+                    if (from < to) v[h] += theirs[first + h * 16 * MV];
+                }
             if (p.gamma) squares += sq[w * MV + i % MV];
         }
         if (split == 1) {
@@ -456,13 +472,13 @@ W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, const int at_once[4]
     // the least split of K with which all tiles are resident at once, a block an SM
     for (int ls = 0; ls < 4 && (1 << ls) <= groups; ++ls) {
         const int most = std::max(1, std::min(ntiles, at_once[ls])), tiles = (ntiles + most - 1) / most;
-        if (tiles > kMaxTiles) continue;
+        if (tiles > (sums_in_act(mv, parts) ? kMaxTiles / 2 : kMaxTiles)) continue;
         const W4Launch c = made(ls, tiles, most);
         if (c.smem <= kBlockSmem) return c;
     }
     // more tiles than that: as many a block as fit, over several rounds of blocks
     for (int ls = 0; ls < 4 && (1 << ls) <= groups; ++ls)
-        for (int tiles = std::min(kMaxTiles, ntiles); tiles >= 1; --tiles) {
+        for (int tiles = std::min(sums_in_act(mv, parts) ? kMaxTiles / 2 : kMaxTiles, ntiles); tiles >= 1; --tiles) {
             const W4Launch c = made(ls, tiles, (ntiles + tiles - 1) / tiles);
             if (c.smem <= kBlockSmem && (tiles >= 2 || ls == 3 || (2 << ls) > groups)) return c;
         }

@@ -68,7 +68,9 @@ def weights(N, K, seed):
 GEMV = [(1, 1, 128, 0, False), (1, 17, 256, 1, True), (1, 160, 4096, 1, False), (2, 48, 1280, 2, True),
         (3, 1026, 2560, 0, True), (4, 500, 384, 0, True), (5, 33, 12288, 1, False), (6, 15, 640, 2, False),
         (7, 16, 128, 2, True), (8, 2560, 9728, 1, False), (1, 9728, 2560, 2, True), (1, 2560, 9728, 1, False),
-        (1, 6144, 2560, 0, True), (8, 8208, 2560, 0, True)]
+        (1, 6144, 2560, 0, True), (8, 8208, 2560, 0, True), (4, 9728, 2560, 2, True), (3, 40, 384, 2, False),
+        (4, 700, 12288, 2, True), (8, 1300, 4096, 2, True), (2, 4001, 9728, 1, False), (1, 30000, 256, 1, False),
+        (4, 20, 2432, 2, False), (8, 33, 2432, 0, True)]
 
 
 @pytest.mark.parametrize("M,N,K,epi,norm", GEMV)
