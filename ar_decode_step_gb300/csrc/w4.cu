@@ -130,7 +130,7 @@ __host__ __device__ inline W4Smem smem_of(int mv, int parts, int tiles, int shar
     const uint32_t outs = tiles * 16 * mv * parts;
     o.act = tiles * parts * 16 * row_pitch(share);
     o.par = o.act + share * act_group_bytes(mv);
-    o.scales = o.par + share * mv * 4;
+    o.scales = (o.par + share * mv * 4 + 15) & ~15u;
     o.sums = o.scales + tiles * parts * share * 32;
     o.sq = o.sums + (sums_in_act(mv, parts) ? 0 : outs * warps * 4);
     o.tot = o.sq + mv * warps * 4;
@@ -181,9 +181,15 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
     auto row_of = [&](int q, int i) {
         return min((tile0 + q / PARTS * step) * 16 + i, p.N - 1) + (q % PARTS) * p.N;
     };
-    // scales, a row a warp at a time, eight rows in flight; the first before the
-    // copies, which would hold them up for 2 us
+    // Scales, bf16 [tile x parts][16][share].  With all of K a tile's are one run of
+    // 32 bytes a group and come with its rows, but for a last tile of fewer rows and
+    // a run that does not start on 16 bytes.  Otherwise a row a warp at a time, eight
+    // rows in flight, the first before the copies, which would hold them up for 2 us.
     __nv_bfloat16* scl = reinterpret_cast<__nv_bfloat16*>(smem + o.scales);
+    auto run_of = [&](int q) { return p.s + (size_t)row_of(q, 0) * groups; };
+    auto in_run = [&](int q) {
+        return split == 1 && (tile0 + q / PARTS * step) * 16 + 16 <= p.N && (reinterpret_cast<uintptr_t>(run_of(q)) & 15) == 0;
+    };
     constexpr int kAhead = 8;
     const int rows = nt * PARTS * 16;
     __nv_bfloat16 sv[kAhead];
@@ -198,23 +204,34 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int i = i0 + j * W;
-            if (i < rows && gl < kg) scl[((i >> 4) * c.share + gl) * 16 + (i & 15)] = sv[j];
+            if (i < rows && gl < kg) scl[i * c.share + gl] = sv[j];
         }
     };
-    load_scales(warp, lane);
+    if (split > 1) load_scales(warp, lane);
     for (int q = warp; q < nt * PARTS; q += W) {
-        if (lane == 0) mbar_arrive_expect_tx(&bars[q], 16 * kg * 64);
+        const bool run = in_run(q);
+        if (lane == 0) mbar_arrive_expect_tx(&bars[q], 16 * kg * 64 + (run ? 32 * groups : 0));
         __syncwarp();
         if (lane < 16)
             bulk_g2s(smem + (size_t)(q * 16 + lane) * pitch, p.W4 + (size_t)row_of(q, lane) * (p.K / 2) + k0 * 64, kg * 64,
                      &bars[q], l2_evict_first_policy());
+        else if (lane == 16 && run)
+            bulk_g2s(scl + (size_t)q * 16 * groups, run_of(q), 32 * groups, &bars[q], l2_evict_first_policy());
     }
-    keep_scales(warp, lane);
-    for (int gl = lane; gl < kg; gl += 32)
-        for (int i0 = gl == lane ? warp + kAhead * W : warp; i0 < rows; i0 += kAhead * W) {
-            load_scales(i0, gl);
-            keep_scales(i0, gl);
-        }
+    if (split > 1) {
+        keep_scales(warp, lane);
+        for (int gl = lane; gl < kg; gl += 32)
+            for (int i0 = gl == lane ? warp + kAhead * W : warp; i0 < rows; i0 += kAhead * W) {
+                load_scales(i0, gl);
+                keep_scales(i0, gl);
+            }
+    } else {
+        for (int q = 0; q < nt * PARTS; ++q)
+            if (!in_run(q))
+                for (int i = warp; i < 16; i += W)
+                    for (int g = lane; g < kg; g += 32)
+                        scl[(q * 16 + i) * c.share + g] = p.s[(size_t)row_of(q, i) * groups + g];
+    }
 
     // a thread adds up output i = its number, + threads, ... at the end: what it
     // adds the first of them to
@@ -316,7 +333,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
         for (int v = 0; v < kVecs; ++v) ap[v] = act_par[g * MV + min(kVecs * t + v, MV - 1)];
         if (kInAct && g == g0) __syncwarp();  // all lanes have read what the sums replace
         const uint8_t* row = smem + r * pitch + t * 16 + g * 64;
-        const __nv_bfloat16* sc = scl + g * 16 + r;
+        const __nv_bfloat16* sc = scl + r * c.share + g;
         float* out = sums + r * MV + kVecs * t;
         // n tiles at a time: their loads, conversions and products are independent
         auto tiles = [&](int q, auto n_) {
@@ -333,7 +350,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
                 wa[k] = *reinterpret_cast<const uint4*>(row + k * 16 * pitch);
                 wb[k] = *reinterpret_cast<const uint4*>(row + (k * 16 + 8) * pitch);
                 sa[k] = __bfloat162float(sc[k * 16 * c.share]);
-                sb[k] = __bfloat162float(sc[k * 16 * c.share + 8]);
+                sb[k] = __bfloat162float(sc[(k * 16 + 8) * c.share]);
             }
             row += n * 16 * pitch;
             sc += n * 16 * c.share;
