@@ -406,6 +406,8 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
     for (int q = 0; q < nt * PARTS; ++q)
         if (g0 == g1 && !mbar_wait(&bars[q], 0)) late = 1;
     __syncthreads();
+    if (late)  // a copy may still be on its way: once more, again with a limit
+        for (int q = 0; q < nt * PARTS; ++q) mbar_wait(&bars[q], 0);
 
     // ---- the warps' sums in order, an output a thread
     const float* all = reinterpret_cast<const float*>(smem + o.sums);
@@ -438,7 +440,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
         } else {
             if (i < MV) tot[i] = squares;
 #pragma unroll
-            for (int h = 0; h < PARTS; ++h) tot[MV + first + h * 16 * MV] = v[h];
+            for (int h = 0; h < PARTS; ++h) tot[MV + first + h * 16 * MV] = late ? NAN : v[h];
         }
     }
     if (split == 1) return;
