@@ -312,20 +312,4 @@ cudaError_t launch_prefill_attention(const float* Q, const __nv_bfloat16* kc, co
 cudaError_t launch_quantize_weight(const __nv_bfloat16* W, int N, int K, uint8_t* W8, float* s,
                                    cudaStream_t st);
 
-// Log probabilities of given codes, entropy and top alternatives (logprobs.cu).
-constexpr int kMaxTop = 32;  // alternatives per codebook, at most
-struct LogprobParams {
-    const float* logits;  // row r, codebook k at logits + r * ld + k * V
-    long long ld;
-    const int* codes;     // [rows][n_cb], or null
-    int rows, n_cb, V;
-    float inv_t;          // 1 / temperature
-    int top;
-    float* logprob;       // [rows][n_cb], or null
-    float* entropy;       // [rows][n_cb], or null
-    int* top_codes;       // [rows][n_cb][top]
-    float* top_logprob;
-};
-cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t s);
-
 }  // namespace tts

@@ -12,7 +12,7 @@
 #include <cmath>
 #include <cstdio>
 
-#include "kernels.h"
+#include "fourbit.cuh"
 #include "tts_decode.h"
 
 namespace tts {

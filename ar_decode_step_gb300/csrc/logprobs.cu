@@ -16,7 +16,7 @@
 
 #include <cooperative_groups.h>
 
-#include "kernels.h"
+#include "fourbit.cuh"
 #include "tts_decode.h"
 
 namespace tts {

@@ -20,6 +20,7 @@
 #include <tuple>
 #include <vector>
 
+#include "fourbit.cuh"
 #include "kernels.h"
 #include "tts_decode.h"
 

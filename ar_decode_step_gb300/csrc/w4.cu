@@ -11,7 +11,7 @@
 
 #include <cooperative_groups.h>
 
-#include "kernels.h"
+#include "fourbit.cuh"
 #include "tts_decode.h"
 
 namespace tts {
