@@ -205,11 +205,11 @@ def attention_decode(qkv, q_norm, k_norm, k_cache, v_cache, out, n_q: int, n_kv:
 # ----------------------------------------------------------------------------
 
 def _check(fn: str, *wanted):
-    """Each of `wanted` is (tensor or None, element bytes, elements): raises
-    TtsError(TTS_ERR_ARG) unless the tensor is a contiguous CUDA tensor of that
-    element size and count (its address and these are all the library sees)."""
-    for t, size, n in wanted:
-        if t is not None and not (t.numel() == n and t.element_size() == size and t.is_cuda and t.is_contiguous()):
+    """Each of `wanted` is (tensor or None, bytes): raises TtsError(TTS_ERR_ARG)
+    unless the tensor is a contiguous CUDA tensor of that many bytes (its address
+    and size are all the library sees)."""
+    for t, n in wanted:
+        if t is not None and (t.nbytes != n or not t.is_cuda or not t.is_contiguous()):
             raise TtsError(fn, -1)
 
 
@@ -222,7 +222,7 @@ def quantize_w4_weight(w_dev, stream=None):
     returns (uint8 [N][K/2], bfloat16 [N][K/128]) device tensors."""
     torch = _torch()
     N, K = w_dev.shape
-    _check("tts_quantize_w4_weight", (w_dev, 2, N * K))
+    _check("tts_quantize_w4_weight", (w_dev, 2 * N * K))
     q = torch.empty((N, K // 2), dtype=torch.uint8, device=w_dev.device)
     s = torch.empty((N, K // 128), dtype=torch.bfloat16, device=w_dev.device)
     _call("tts_quantize_w4_weight", w_dev.data_ptr(), N, K, q.data_ptr(), s.data_ptr(), stream)
@@ -238,8 +238,8 @@ def gemv_w4(x_dev, w4_dev, s_dev, y_dev, epi: int = 0, resid_dev=None, gamma_dev
     M, K = x_dev.shape
     N = y_dev.shape[-1]
     rows = 2 * N if epi == 2 else N
-    _check("tts_gemv_w4", (x_dev, 4, M * K), (w4_dev, 1, rows * (K // 2)), (s_dev, 2, rows * (K // 128)),
-           (y_dev, 4, M * N), (resid_dev, 4, M * N), (gamma_dev, 2, K))
+    _check("tts_gemv_w4", (x_dev, 4 * M * K), (w4_dev, rows * (K // 2)), (s_dev, 2 * rows * (K // 128)),
+           (y_dev, 4 * M * N), (resid_dev, 4 * M * N), (gamma_dev, 2 * K))
     _call("tts_gemv_w4", x_dev.data_ptr(), w4_dev.data_ptr(), s_dev.data_ptr(), _opt(resid_dev), _opt(gamma_dev),
           y_dev.data_ptr(), M, N, K, epi, eps, stream)
 
@@ -247,7 +247,7 @@ def gemv_w4(x_dev, w4_dev, s_dev, y_dev, epi: int = 0, resid_dev=None, gamma_dev
 def _check_kv4(fn: str, k4, v4, k_par, v_par):
     n_kv, max_pos, _ = k4.shape
     rows = n_kv * max_pos
-    _check(fn, (k4, 1, rows * 64), (v4, 1, rows * 64), (k_par, 2, rows * 4), (v_par, 2, rows * 4))
+    _check(fn, (k4, rows * 64), (v4, rows * 64), (k_par, 2 * rows * 4), (v_par, 2 * rows * 4))
     return n_kv, max_pos
 
 
@@ -257,7 +257,7 @@ def quantize_kv4(k_dev, v_dev, k4, v4, k_par, v_par, p0: int, p1: int, stream=No
     [n_kv][max_pos][2][2]."""
     n_kv, max_pos = _check_kv4("tts_quantize_kv4", k4, v4, k_par, v_par)
     stride = k_dev.shape[1]
-    _check("tts_quantize_kv4", (k_dev, 2, n_kv * stride * 128), (v_dev, 2, n_kv * stride * 128))
+    _check("tts_quantize_kv4", (k_dev, 2 * n_kv * stride * 128), (v_dev, 2 * n_kv * stride * 128))
     _call("tts_quantize_kv4", k_dev.data_ptr(), v_dev.data_ptr(), n_kv, p0, p1, stride, k4.data_ptr(), v4.data_ptr(),
           k_par.data_ptr(), v_par.data_ptr(), max_pos, stream)
 
@@ -267,7 +267,7 @@ def dequantize_kv4(k4, v4, k_par, v_par, k_dev, v_dev, p0: int, p1: int, stream=
     bf16 caches [n_kv][stride][128]."""
     n_kv, max_pos = _check_kv4("tts_dequantize_kv4", k4, v4, k_par, v_par)
     stride = k_dev.shape[1]
-    _check("tts_dequantize_kv4", (k_dev, 2, n_kv * stride * 128), (v_dev, 2, n_kv * stride * 128))
+    _check("tts_dequantize_kv4", (k_dev, 2 * n_kv * stride * 128), (v_dev, 2 * n_kv * stride * 128))
     _call("tts_dequantize_kv4", k4.data_ptr(), v4.data_ptr(), k_par.data_ptr(), v_par.data_ptr(), n_kv, p0, p1,
           max_pos, k_dev.data_ptr(), v_dev.data_ptr(), stride, stream)
 
@@ -289,8 +289,8 @@ def attention_decode_kv4(qkv, q_norm, k_norm, k4, v4, k_par, v_par, out, n_q: in
     or None."""
     heads, max_pos = _check_kv4("tts_attention_decode_kv4", k4, v4, k_par, v_par)
     ws_bytes = workspace.numel()
-    _check("tts_attention_decode_kv4", (qkv, 4, (n_q + 2 * n_kv) * 128), (q_norm, 2, 128), (k_norm, 2, 128),
-           (out, 4, n_q * 128), (kv_row, 4, 2 * n_kv * 128), (workspace, 1, ws_bytes))
+    _check("tts_attention_decode_kv4", (qkv, 4 * (n_q + 2 * n_kv) * 128), (q_norm, 2 * 128), (k_norm, 2 * 128),
+           (out, 4 * n_q * 128), (kv_row, 4 * 2 * n_kv * 128), (workspace, ws_bytes))
     if heads != n_kv:
         raise TtsError("tts_attention_decode_kv4", -1)
     _call("tts_attention_decode_kv4", qkv.data_ptr(), q_norm.data_ptr(), k_norm.data_ptr(), k4.data_ptr(),
@@ -304,7 +304,7 @@ def code_logprobs(logits, codes, cb_vocab: int, top: int = 0, temperature: float
     top_codes [rows][n_cb][top], top_logprob [rows][n_cb][top])."""
     torch = _torch()
     rows, n_cb = codes.shape
-    _check("tts_code_logprobs", (codes, 4, rows * n_cb))
+    _check("tts_code_logprobs", (codes, 4 * rows * n_cb))
     if not (logits.is_cuda and logits.dtype is torch.float32 and logits.dim() == 2 and logits.shape[0] == rows
             and logits.shape[1] >= n_cb * cb_vocab and logits.stride(1) == 1):
         raise TtsError("tts_code_logprobs", -1)
