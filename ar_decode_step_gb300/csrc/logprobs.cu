@@ -70,33 +70,43 @@ __device__ __forceinline__ Part join_lanes(Part a, float c) {
     return a;
 }
 
-// Up to 64 candidates for the alternatives; a sorted list of up to 32 uses the first half.
+// An entry above -inf as one number that orders as the alternatives do: value
+// first, then the lower number.
+typedef unsigned long long Entry;
+__device__ __forceinline__ Entry entry_of(float v, int i) { return (Entry)ranked(v) << 32 | (uint32_t)~i; }
+__device__ __forceinline__ float entry_value(Entry e) { return from_ranked((uint32_t)(e >> 32)); }
+__device__ __forceinline__ int entry_number(Entry e) { return (int)~(uint32_t)e; }
+
+// Up to 64 candidates for the alternatives, then a sorted list of up to 32 (0: none).
 struct Candidates {
-    float v[64];
-    int i[64];
+    Entry e[64];
 };
-// The `top` (at most 32) largest of n <= 64 candidates, all above -inf, largest
-// first, equal ones by number: lane k gets the k-th.
-__device__ __forceinline__ void sort_candidates(const Candidates& c, int n, int top, float& list_v, int& list_i) {
+// The `top` (at most 32) largest of n <= 64 candidates, all different, largest
+// first: lane k gets the k-th.  An entry's place is the number of those above it:
+// four instructions a candidate, none waiting for another.
+__device__ __forceinline__ void sort_candidates(Candidates& c, int n, int top, float& list_v, int& list_i) {
     const int lane = threadIdx.x & 31;
-    // two a lane, the better one first
-    uint32_t key = lane < n ? ranked(c.v[lane]) : 0u, key2 = lane + 32 < n ? ranked(c.v[lane + 32]) : 0u;
-    int at = lane < n ? c.i[lane] : INT_MAX, at2 = lane + 32 < n ? c.i[lane + 32] : INT_MAX;
-    if (key2 > key || (key2 == key && at2 < at)) {
-        const uint32_t k = key;
-        const int i = at;
-        key = key2, at = at2, key2 = k, at2 = i;
-    }
-    list_v = -INFINITY;
-    for (int k = 0; k < top; ++k) {
-        const uint32_t most = __reduce_max_sync(kAll, key);
-        if (most <= kRankedNone) break;
-        const int win = __reduce_min_sync(kAll, key == most ? at : INT_MAX);
-        if (key == most && at == win) key = key2, at = at2, key2 = 0u;
-        if (lane == k) {
-            list_v = from_ranked(most);
-            list_i = win;
+    const Entry a = lane < n ? c.e[lane] : 0, b = lane + 32 < n ? c.e[lane + 32] : 0;
+    int place_a = 0, place_b = 0;
+    if (n <= 32) {
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) place_a += c.e[j] > a;
+    } else {
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+            const Entry other = c.e[j];
+            place_a += other > a;
+            place_b += other > b;
         }
+    }
+    __syncwarp();
+    if (a && place_a < top) c.e[place_a] = a;
+    if (b && place_b < top) c.e[place_b] = b;
+    __syncwarp();
+    list_v = -INFINITY;
+    if (lane < min(n, top)) {
+        list_v = entry_value(c.e[lane]);
+        list_i = entry_number(c.e[lane]);
     }
 }
 
@@ -220,10 +230,7 @@ __device__ __forceinline__ Part warp_run(const float* z, int n, int first, float
             int place = 0;
             auto gather = [&](bool in, float x, int at) {
                 const unsigned who = __ballot_sync(kAll, in);
-                if (in) {
-                    cand.v[place + __popc(who & ((1u << lane) - 1))] = x;
-                    cand.i[place + __popc(who & ((1u << lane) - 1))] = at;
-                }
+                if (in) cand.e[place + __popc(who & ((1u << lane) - 1))] = entry_of(x, at);
                 place += __popc(who);
             };
             if (LISTED) gather(old_v >= bound, old_v, old_i);
@@ -292,25 +299,23 @@ __device__ __forceinline__ Part warp_run(const float* z, int n, int first, float
     return r;
 }
 
-// n <= 32 sorted lists merged: lane k gets the k-th entry of all, equal ones by number.
+// n <= 32 sorted lists merged: lane k gets the k-th entry of all.
 __device__ __forceinline__ void merge_lists(const Candidates* lists, int n, int top, float& list_v, int& list_i) {
     const int lane = threadIdx.x & 31;
     int next = 0;
-    float head_v = lane < n ? lists[lane].v[0] : -INFINITY;
-    int head_i = lane < n ? lists[lane].i[0] : INT_MAX;
+    Entry head = lane < n ? lists[lane].e[0] : 0;
     list_v = -INFINITY;
     for (int k = 0; k < top; ++k) {
-        const uint32_t key = ranked(head_v), most = __reduce_max_sync(kAll, key);
-        if (most <= kRankedNone) break;
-        const int win = __reduce_min_sync(kAll, key == most ? head_i : INT_MAX);
+        const uint32_t value = (uint32_t)(head >> 32), most = __reduce_max_sync(kAll, value);
+        if (most == 0) break;
+        const uint32_t win = __reduce_max_sync(kAll, value == most ? (uint32_t)head : 0u);
         if (lane == k) {
             list_v = from_ranked(most);
-            list_i = win;
+            list_i = (int)~win;
         }
-        if (key == most && head_i == win) {
+        if (value == most && (uint32_t)head == win) {
             ++next;
-            head_v = next < 32 ? lists[lane].v[next] : -INFINITY;
-            head_i = next < 32 ? lists[lane].i[next] : INT_MAX;
+            head = next < 32 ? lists[lane].e[next] : 0;
         }
     }
 }
@@ -388,8 +393,7 @@ __global__ void __launch_bounds__(kLongWarps * 32) logprobs_long_kernel(const Lo
     for (int first = ((int)blockIdx.y * W + warp) * kRun; first < p.V; first += C * W * kRun)
         r = join(r, warp_run<kRunNv, true>(z + first, min(kRun, p.V - first), first, c, p.top, lists[warp], list_v, list_i), c);
     if (lane == 0) parts[warp] = r;
-    lists[warp].v[lane] = list_v;
-    lists[warp].i[lane] = list_i;
+    lists[warp].e[lane] = list_v == -INFINITY ? 0 : entry_of(list_v, list_i);
     if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     __syncthreads();
     if (warp == 0) {
@@ -401,8 +405,7 @@ __global__ void __launch_bounds__(kLongWarps * 32) logprobs_long_kernel(const Lo
             const auto cluster = cg::this_cluster();
             const unsigned at = blockIdx.y;
             if (lane == 0) *cluster.map_shared_rank(&block_part[at], 0) = r;
-            *cluster.map_shared_rank(&block_list[at].v[lane], 0) = list_v;
-            *cluster.map_shared_rank(&block_list[at].i[lane], 0) = list_i;
+            *cluster.map_shared_rank(&block_list[at].e[lane], 0) = list_v == -INFINITY ? 0 : entry_of(list_v, list_i);
         }
     }
     if (C == 1) return;
