@@ -8,7 +8,9 @@ namespace tts {
 // Launch with a programmatic edge from the kernel before it in the stream.
 // The kernel triggers at its start and waits before its first access to global
 // memory, so its blocks may start as soon as an SM is free while every memory
-// access stays in stream order.  Clusters of cluster_y x cluster_z blocks.
+// access stays in stream order.  Its loads are ordinary ones: the read-only path
+// wants memory that nobody writes while the kernel runs, its wait included.
+// Clusters of cluster_y x cluster_z blocks.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_ordered(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster_y,
                                   int cluster_z, Args... args) {

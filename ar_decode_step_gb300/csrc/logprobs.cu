@@ -5,7 +5,7 @@
 // A warp takes a run of up to 32 NV entries of a row into registers, lane l the
 // entries l, l + 32, ..., and finds there the maximum, the sums of e^z and
 // z e^z relative to it, and the `top` largest entries, without a second
-// reading.  A row of up to 1056 entries is one warp's (eight rows a block); a
+// reading.  A row of up to 1056 entries is one warp's (four rows a block); a
 // longer one is shared by the warps of a block, or by a cluster of blocks when
 // there are few rows, whose results are joined through shared memory in a
 // fixed order, as a softmax over parts is.
@@ -26,7 +26,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kRunNv = 33;                // 33 values a lane: 1026-entry codebooks in one run
 constexpr int kRun = 32 * kRunNv;
-constexpr int kShortWarps = 8;            // rows a block, short rows
+// Rows a block, short rows: blocks of 4 leave an SM's registers least idle (4096
+// frames x 8 x 1026, 5 alternatives: 29.7 us; 8 rows 30.1, 16 rows 33.5).
+constexpr int kShortWarps = 4;
 constexpr int kLongWarps = 16;            // warps a block, at most, long rows
 
 __device__ __forceinline__ float ex2(float x) {
@@ -122,7 +124,7 @@ __device__ __forceinline__ void sort_candidates(Candidates& c, int n, int top, f
 // that fails (ties across the bound), with a NaN in the run, or where fewer than
 // `top` lanes have an entry above -inf, they are taken out one by one instead.
 // (One by one throughout took 41 us on 4096 frames x 8 x 1026 with 5 alternatives
-// and 158 us with 32; without alternatives the same frames take 22 us.)
+// and 158 us with 32; now 30 and 64, and 22 without alternatives.)
 template <int NV, bool LISTED>  // LISTED: it comes with a list
 __device__ __forceinline__ Part warp_run(const float* z, int n, int first, float c, int top, Candidates& cand,
                                          float& list_v, int& list_i) {
@@ -130,13 +132,15 @@ __device__ __forceinline__ Part warp_run(const float* z, int n, int first, float
     float v[NV + (NV & 1)];
     if (n >= 32 * (NV - 1)) {  // all but the last load unguarded
 #pragma unroll
-        for (int i = 0; i < NV - 1; ++i) v[i] = __ldcs(z + lane + 32 * i);
-        v[NV - 1] = lane + 32 * (NV - 1) < n ? __ldcs(z + lane + 32 * (NV - 1)) : -INFINITY;
+        for (int i = 0; i < NV - 1; ++i) v[i] = z[lane + 32 * i];
+        v[NV - 1] = lane + 32 * (NV - 1) < n ? z[lane + 32 * (NV - 1)] : -INFINITY;
     } else {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = lane + 32 * i < n ? __ldcs(z + lane + 32 * i) : -INFINITY;
+        for (int i = 0; i < NV; ++i) v[i] = lane + 32 * i < n ? z[lane + 32 * i] : -INFINITY;
     }
     if (NV & 1) v[NV] = -INFINITY;
+    // (Loads marked as read once were 2 % faster without alternatives and 12 % slower
+    // with 20, which read theirs again.)
     // maxima of chunks of 8 (a NaN is passed over)
     constexpr int kChunks = (NV + 7) / 8;
     float cm[kChunks];
