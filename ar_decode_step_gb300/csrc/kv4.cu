@@ -8,9 +8,9 @@
 // in byte 8r + 4 + j: eight units of 8 bytes, each with one 32-bit word per
 // half.  Parameters: bf16 [n_kv][max_pos][2][2], (s, m) per half.
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <mutex>
 
 #include "fourbit.cuh"
 #include "tts_decode.h"
@@ -40,6 +40,7 @@ struct Kv4Params {
     int n_q, n_kv, max_pos, pos;
     float eps;
     int S, tiles_per_split;  // splits per kv head, tiles of 16 cached positions per split
+    int cluster;             // a head's splits are a cluster, joined through shared memory
     unsigned* tickets;       // [n_kv], zero between calls
     float2* part_ml;         // [n_kv][S][G] maximum, sum
     float* part_o;           // [n_kv][S][G][128]
@@ -289,7 +290,10 @@ __device__ __forceinline__ void norm_rope_exact(float4 x4, uint2 gb, const float
 // A block takes one kv head and one contiguous range of 16-position tiles (a
 // split); its warps take the range's tiles in turn, each with its own ring of
 // asynchronous copies, running maximum, sum and output, so nothing in the loop
-// waits for another warp.
+// waits for another warp.  The partials are joined in a fixed order: a block's
+// warps in its shared memory, and the blocks of a head, where they are a cluster, by
+// writing each a share of the channels into one another's shared memory, else
+// through the workspace by the last block to finish.
 //
 // Both products run on the tensor cores (m16n8k16, fp16 operands, fp32 sums).
 // Codes enter centred, u - 8 and, from a whole byte, (u - 8) + 16 (u' - 8), exact
@@ -322,6 +326,9 @@ constexpr int kStagePar = 2 * kStageV;                    // then K and V parame
 constexpr int kStageBytes = kStagePar + 2 * kTilePos * 8;
 constexpr int kRingBytes = kStages * kStageBytes;         // per warp
 constexpr int kAttnSmem = kAttnWarps * kRingBytes;
+constexpr int kMaxCluster = 16;    // blocks of a cluster, at most
+constexpr int kOneBlockTiles = 12;  // a head of up to so many tiles is one block's
+constexpr int kClusterTiles = 4;    // tiles a block of a cluster, at least
 static_assert(kRingBytes >= 8 * kHeadDim * 4, "a warp's output partial reuses its ring");
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
@@ -429,6 +436,21 @@ struct LaneCopy {
     }
 };
 
+// To the same place in the shared memory of block `rank` of the cluster.
+__device__ __forceinline__ uint32_t remote(const void* at, int rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(at)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void store_remote(float2* at, int rank, float2 v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(remote(at, rank)), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void store_remote(float4* at, int rank, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(remote(at, rank)), "f"(v.x), "f"(v.y), "f"(v.z),
+                 "f"(v.w)
+                 : "memory");
+}
+
 template <int G>
 __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __grid_constant__ Kv4Params p) {
     extern __shared__ __align__(128) uint8_t ring[];
@@ -443,12 +465,16 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
     __shared__ float merge_c[kMaxSplitUnits][G];      // a partial's weight in the merge
     __shared__ float merge_l[G];
     __shared__ int s_last;
+    // a cluster's partials of this block's share of the outputs
+    __shared__ __align__(16) float4 box_o[G * kHeadDim / 4 + kMaxCluster];
+    __shared__ float2 box_ml[kMaxCluster][G];
 
     // the warp's number by a shuffle: the compiler then keeps the loop's control in
     // uniform registers
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int r = lane >> 2, t = lane & 3;
-    const int g = blockIdx.x / p.S, split = blockIdx.x % p.S;
+    const int g = blockIdx.x, split = blockIdx.y;
+    if (p.cluster) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const bool has_new = split == p.S - 1;
     const size_t base = (size_t)g * p.max_pos;
     const int tile_end = min((p.pos + kTilePos - 1) / kTilePos, (split + 1) * p.tiles_per_split);
@@ -816,6 +842,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
         }
     }
     __syncthreads();
+    // all blocks of the cluster run: their shared memory may be written
+    if (p.cluster) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 
     // ---- merge the warps and the new row, in order.  A partial with sum 0 is
     // empty; NaN sums pass through.
@@ -830,11 +858,13 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
         if (in) merge_c[lane][warp] = c;
         if (lane == 0) {
             merge_l[warp] = L;
-            if (p.S > 1) p.part_ml[unit * G + warp] = make_float2(mx, L);
+            if (p.S > 1 && !p.cluster) p.part_ml[unit * G + warp] = make_float2(mx, L);
         }
+        if (p.cluster && lane < p.S) store_remote(&box_ml[split][warp], lane, make_float2(mx, L));
     }
     __syncthreads();
     constexpr int kVec = G * kHeadDim / 4;  // the group's outputs, four a thread
+    const int share = p.cluster ? (kVec + p.S - 1) / p.S : kVec;
     if (threadIdx.x < kVec) {
         const int j = threadIdx.x / (kHeadDim / 4), d4 = threadIdx.x % (kHeadDim / 4);
         float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -852,11 +882,39 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
         if (p.S == 1) {
             const float L = merge_l[j];
             reinterpret_cast<float4*>(p.out)[(size_t)g * kVec + threadIdx.x] = make_float4(O.x / L, O.y / L, O.z / L, O.w / L);
+        } else if (p.cluster) {
+            const int to = threadIdx.x / share;
+            store_remote(&box_o[split * share + threadIdx.x - to * share], to, O);
         } else {
             reinterpret_cast<float4*>(p.part_o)[unit * kVec + threadIdx.x] = O;
         }
     }
     if (p.S == 1) return;
+
+    // ---- a cluster: each block joins its share of the outputs, in order
+    if (p.cluster) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        const int vec = split * share + threadIdx.x;
+        if (threadIdx.x < share && vec < kVec) {
+            const int j = vec / (kHeadDim / 4);
+            float mx = -INFINITY, L = 0.f;
+            for (int s = 0; s < p.S; ++s) mx = fmaxf(mx, box_ml[s][j].x);
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s = 0; s < p.S; ++s) {
+                const float2 ml = box_ml[s][j];
+                const float4 v = box_o[s * share + threadIdx.x];
+                const float c = ex2(ml.x - mx);
+                L = fmaf(ml.y, c, L);
+                O.x = fmaf(v.x, c, O.x);
+                O.y = fmaf(v.y, c, O.y);
+                O.z = fmaf(v.z, c, O.z);
+                O.w = fmaf(v.w, c, O.w);
+            }
+            reinterpret_cast<float4*>(p.out)[(size_t)g * kVec + vec] = make_float4(O.x / L, O.y / L, O.z / L, O.w / L);
+        }
+        return;
+    }
 
     // ---- the last split of this kv head to finish merges all splits, in order
     __syncthreads();
@@ -945,19 +1003,70 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
     if (threadIdx.x == 0) p.tickets[g] = 0u;
 }
 
+int max_splits(int n_kv) { return n_kv >= kMaxSplitUnits ? 1 : kMaxSplitUnits / n_kv; }
+
 template <int G>
-cudaError_t launch_attn_kv4(const Kv4Params& p, cudaStream_t s) {
-    static std::atomic<unsigned long long> ready{0};  // devices whose shared-memory limit is raised
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(attn_kv4_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(bit, std::memory_order_relaxed);
+cudaError_t launch_attn_kv4(Kv4Params p, int dev, int sms, cudaStream_t s) {
+    // per device: the shared-memory limit raised, and how many clusters of 2 .. 16
+    // blocks run at once (a cluster stays within a group of SMs; above 8 blocks is
+    // this device's own, so it is asked for)
+    static std::mutex mu;
+    static int at_once_of[64][kMaxCluster + 1] = {};
+    const auto kern = attn_kv4_kernel<G>;
+    int at_once[kMaxCluster + 1];
+    {
+        const std::lock_guard<std::mutex> lock(mu);
+        int* v = at_once_of[dev & 63];
+        if (!v[1]) {
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
+            if (e != cudaSuccess) return e;
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            int n[kMaxCluster + 1] = {0, sms};
+            for (int c = 2; c <= kMaxCluster; ++c) {
+                cudaLaunchConfig_t q = {};
+                q.gridDim = dim3(1, c);
+                q.blockDim = dim3(kAttnWarps * 32);
+                q.dynamicSmemBytes = kAttnSmem;
+                cudaLaunchAttribute at[1];
+                at[0].id = cudaLaunchAttributeClusterDimension;
+                at[0].val.clusterDim.x = 1;
+                at[0].val.clusterDim.y = c;
+                at[0].val.clusterDim.z = 1;
+                q.attrs = at;
+                q.numAttrs = 1;
+                e = cudaOccupancyMaxActiveClusters(&n[c], kern, &q);
+                if (e != cudaSuccess) return e;
+            }
+            std::copy(n, n + kMaxCluster + 1, v);
+        }
+        std::copy(v, v + kMaxCluster + 1, at_once);
     }
-    return launch_ordered(attn_kv4_kernel<G>, dim3(p.n_kv * p.S), dim3(kAttnWarps * 32), kAttnSmem, s, 1, 1, p);
+    // How a head's cache is split, none empty (us a call at 32/8 heads unless said):
+    // - up to 192 positions one block takes it: 4.3 at 100 against 5.0 in two
+    //   blocks, 5.05 at 200 against 4.9 in four;
+    // - then a cluster, whose blocks join through shared memory, four tiles a
+    //   block up to the largest cluster that all heads find room for at once: 5.1 at
+    //   300 (one block 5.6, blocks of eight tiles 5.2), 5.5 at 1280 (joined through
+    //   global memory 7.4, blocks of 16 tiles in clusters of at most eight 6.6);
+    // - and where that leaves a warp more than two tiles, blocks all over the
+    //   device, a tile a warp, joined through global memory: 8.5 at 8000
+    //   positions against 8.7, but 7.8 at 5000 against 7.5.  Eight queries a head, with
+    //   partials twice as large, break even at three tiles (14000, 16/2 heads).
+    const int tiles = (p.pos + kTilePos - 1) / kTilePos;
+    int S = 1;
+    if (tiles > kOneBlockTiles) {
+        int most = 1;
+        for (int c = 2; c <= kMaxCluster; ++c)
+            if (at_once[c] >= p.n_kv) most = c;
+        S = std::min(most, (tiles + kClusterTiles - 1) / kClusterTiles);
+        p.cluster = S > 1 && tiles <= S * kAttnWarps * (G == 8 ? 3 : 2);
+        if (!p.cluster)
+            S = std::max(1, std::min({(tiles + kAttnWarps - 1) / kAttnWarps, max_splits(p.n_kv), sms / p.n_kv}));
+    }
+    p.tiles_per_split = std::max(1, (tiles + S - 1) / S);
+    p.S = std::max(1, (tiles + p.tiles_per_split - 1) / p.tiles_per_split);
+    return launch_ordered(kern, dim3(p.n_kv, p.S), dim3(kAttnWarps * 32), kAttnSmem, s, p.cluster ? p.S : 1, 1, p);
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -971,7 +1080,6 @@ int report_kv4(cudaError_t e, const char* what) {
     return TTS_ERR_CUDA;
 }
 
-int max_splits(int n_kv) { return n_kv >= kMaxSplitUnits ? 1 : kMaxSplitUnits / n_kv; }
 
 // [tickets][outputs: 128 words per split and query head][maximum and sum: 2
 // words per split and query head].  The tickets' place does not depend on the
@@ -1103,16 +1211,6 @@ extern "C" int tts_attention_decode_kv4(const float* qkv, const void* q_norm, co
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return TTS_ERR_CUDA;
-    // splits: at most one block per SM over all kv heads, a tile for every warp
-    // of a block, none empty.  Up to two tiles a warp one block takes the whole
-    // head: 300 positions in 6.4 us against 7.0 in two blocks, whose merge costs
-    // more than the second round of tiles; 700 positions take 8.1 us in two
-    // blocks and 7.5 in three.
-    const int tiles = (pos + kTilePos - 1) / kTilePos;
-    int S = tiles <= 2 * kAttnWarps ? 1 : (tiles + kAttnWarps - 1) / kAttnWarps;
-    S = std::max(1, std::min(S, std::min(max_splits(n_kv), sms / n_kv)));
-    p.tiles_per_split = std::max(1, (tiles + S - 1) / S);
-    p.S = std::max(1, (tiles + p.tiles_per_split - 1) / p.tiles_per_split);
     char* ws = static_cast<char*>(workspace);
     p.tickets = reinterpret_cast<unsigned*>(ws);
     p.part_o = reinterpret_cast<float*>(ws + kTicketBytes);  // 16-byte vectors: before the 8-byte ones
@@ -1120,10 +1218,10 @@ extern "C" int tts_attention_decode_kv4(const float* qkv, const void* q_norm, co
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     switch (n_q / n_kv) {
-        case 1: e = launch_attn_kv4<1>(p, st); break;
-        case 2: e = launch_attn_kv4<2>(p, st); break;
-        case 4: e = launch_attn_kv4<4>(p, st); break;
-        default: e = launch_attn_kv4<8>(p, st); break;
+        case 1: e = launch_attn_kv4<1>(p, dev, sms, st); break;
+        case 2: e = launch_attn_kv4<2>(p, dev, sms, st); break;
+        case 4: e = launch_attn_kv4<4>(p, dev, sms, st); break;
+        default: e = launch_attn_kv4<8>(p, dev, sms, st); break;
     }
     return e == cudaSuccess ? TTS_OK : report_kv4(e, "tts_attention_decode_kv4");
 }

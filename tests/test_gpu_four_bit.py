@@ -356,6 +356,60 @@ def test_attention_kv4_streams_and_graphs(ads):
             c.check("shared workspace")
 
 
+# Cached positions at which the way a head's cache is divided changes (one block, a
+# cluster of blocks of two to sixteen, blocks joined through the workspace), for
+# each number of queries a head, with shares of the channels that do not come
+# out even.
+DIVIDED = [(32, 8, 192), (32, 8, 193), (32, 8, 2047), (32, 8, 6144), (32, 8, 6145), (4, 1, 8192), (4, 1, 8193),
+           (8, 1, 12288), (8, 1, 12289), (16, 2, 2900), (2, 2, 3900), (2, 2, 8300), (12, 6, 1800), (6, 3, 9100),
+           (16, 16, 1000), (33, 33, 700), (9, 9, 5000), (160, 40, 900)]
+
+
+@pytest.mark.parametrize("n_q,n_kv,pos", DIVIDED)
+def test_attention_kv4_however_a_head_is_divided(ads, n_q, n_kv, pos):
+    import torch
+    a = Attn(ads, n_q, n_kv, pos + 3, pos)
+    a.call()
+    a.check()
+    first = a.out.clone()
+    for _ in range(3):
+        a.out.fill_(np.nan)
+        a.call()
+        assert torch.equal(first, a.out)
+
+
+def test_attention_kv4_long_caches_in_two_graphs(ads):
+    """Calls that join through their workspaces, two captured and replayed at once on
+    two streams, then a short and a long one in turn over one workspace."""
+    import torch
+    pair = Attn(ads, 32, 8, 9001, 9000, seed=91), Attn(ads, 16, 2, 14501, 14500, seed=96)
+    for x in pair:
+        x.call()
+    torch.cuda.synchronize()
+    streams, graphs = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for x, s in zip(pair, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            x.call(stream=s.cuda_stream)
+            x.call(stream=s.cuda_stream)
+        graphs.append(g)
+        x.out.fill_(np.nan)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for x in pair:
+        x.check("graph")
+    shared = torch.zeros(ads.kv4_workspace_bytes(32, 8), dtype=torch.uint8, device="cuda")
+    for n_q, n_kv, pos in ((32, 8, 500), (4, 1, 9000), (32, 8, 7000), (32, 8, 100), (8, 4, 12000)):
+        c = Attn(ads, n_q, n_kv, pos + 1, pos)
+        c.ws = shared
+        c.call()
+        c.check("shared workspace")
+
+
 # ---- a decoder layer of them ---------------------------------------------------------------
 
 def test_layer_of_four_bit_operators(ads):
