@@ -31,6 +31,24 @@ inline cudaError_t launch_ordered(void (*kern)(KArgs...), dim3 grid, dim3 block,
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// How many clusters of cluster_y x cluster_z such blocks run at once (a cluster
+// stays within a group of SMs, so fewer than SMs / blocks).
+template <typename Kernel>
+inline cudaError_t clusters_at_once(Kernel kern, int threads, size_t smem, int cluster_y, int cluster_z, int* n) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1, cluster_y, cluster_z);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 1;
+    at[0].val.clusterDim.y = cluster_y;
+    at[0].val.clusterDim.z = cluster_z;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(n, kern, &cfg);
+}
+
 // 4-bit codes as operands of fp16 products.  Each 16-bit half of w holds two bytes of
 // two codes: nibble_bytes takes byte 0 of both halves (odd = 0) or byte 1 to the
 // low byte of a half under 0x64, which reads as the fp16 value 1024 + byte.

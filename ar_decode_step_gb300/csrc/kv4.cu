@@ -1024,18 +1024,7 @@ cudaError_t launch_attn_kv4(Kv4Params p, int dev, int sms, cudaStream_t s) {
             if (e != cudaSuccess) return e;
             int n[kMaxCluster + 1] = {0, sms};
             for (int c = 2; c <= kMaxCluster; ++c) {
-                cudaLaunchConfig_t q = {};
-                q.gridDim = dim3(1, c);
-                q.blockDim = dim3(kAttnWarps * 32);
-                q.dynamicSmemBytes = kAttnSmem;
-                cudaLaunchAttribute at[1];
-                at[0].id = cudaLaunchAttributeClusterDimension;
-                at[0].val.clusterDim.x = 1;
-                at[0].val.clusterDim.y = c;
-                at[0].val.clusterDim.z = 1;
-                q.attrs = at;
-                q.numAttrs = 1;
-                e = cudaOccupancyMaxActiveClusters(&n[c], kern, &q);
+                e = clusters_at_once(kern, kAttnWarps * 32, kAttnSmem, c, 1, &n[c]);
                 if (e != cudaSuccess) return e;
             }
             std::copy(n, n + kMaxCluster + 1, v);

@@ -488,13 +488,28 @@ W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, const int at_once[4]
         return W4Launch{warps, tiles, share, log_split, grid, ((1ull << 32) + warps - 1) / warps,
                         smem_of(mv, parts, tiles, share, warps).total};
     };
-    // the least split of K with which all tiles are resident at once, a block an SM
+    // All tiles resident at once, a block an SM, K split so that the estimate is
+    // least: a warp's turns (groups of K, between the most a warp has and the mean)
+    // times its tiles and the preparation of its vectors, and 2.2 tiles for joining
+    // a cluster.  2560 x 9728 at 1, 2, 4 vectors: K in four 7.7, 7.7, 7.9 us, the least
+    // split that fits 8.0, 8.7, 9.2; 2560 x 4096: K whole 4.7, 5.0, 5.4 against 5.4, 5.4, 5.7
+    // in two, at 8 vectors 7.8 against 7.1.  (Clusters of 3, 5 and 6 blocks were
+    // slower than of 4 and 8 throughout.)
+    W4Launch best{};
+    float least = 0.f;
     for (int ls = 0; ls < 4 && (1 << ls) <= groups; ++ls) {
         const int most = std::max(1, std::min(ntiles, at_once[ls])), tiles = (ntiles + most - 1) / most;
         if (tiles > (sums_in_act(mv, parts) ? kMaxTiles / 2 : kMaxTiles)) continue;
         const W4Launch c = made(ls, tiles, most);
-        if (c.smem <= kBlockSmem) return c;
+        if (c.smem > kBlockSmem) continue;
+        const float turns = 0.5f * ((float)((c.share + c.warps - 1) / c.warps) + (float)c.share / (float)c.warps);
+        const float cost = turns * ((float)(tiles * parts) + 0.22f * (float)mv) + (ls > 0 ? 2.2f : 0.f);
+        if (!best.warps || cost < least) {
+            best = c;
+            least = cost;
+        }
     }
+    if (best.warps) return best;
     // more tiles than that: as many a block as fit, over several rounds of blocks
     for (int ls = 0; ls < 4 && (1 << ls) <= groups; ++ls)
         for (int tiles = std::min(sums_in_act(mv, parts) ? kMaxTiles / 2 : kMaxTiles, ntiles); tiles >= 1; --tiles) {
@@ -507,8 +522,7 @@ W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, const int at_once[4]
 template <int MV, int PARTS>
 cudaError_t launch_gemv_w4_as(const W4Params& p, int dev, int sms, cudaStream_t s) {
     // per device: the shared-memory limit raised, and how many clusters of 1, 2, 4
-    // and 8 blocks run at once with a block an SM (a cluster stays within a group
-    // of SMs, so fewer than SMs / blocks)
+    // and 8 blocks run at once with a block an SM
     static std::mutex mu;
     static int at_once_of[64][4] = {};
     const auto kern = gemv_w4_kernel<MV, PARTS>;
@@ -521,18 +535,7 @@ cudaError_t launch_gemv_w4_as(const W4Params& p, int dev, int sms, cudaStream_t 
             if (e != cudaSuccess) return e;
             int n[4] = {sms, 0, 0, 0};
             for (int ls = 1; ls < 4; ++ls) {
-                cudaLaunchConfig_t q = {};
-                q.gridDim = dim3(sms, 1, 1 << ls);
-                q.blockDim = dim3(max_warps(MV) * 32);
-                q.dynamicSmemBytes = kBlockSmem;
-                cudaLaunchAttribute at[1];
-                at[0].id = cudaLaunchAttributeClusterDimension;
-                at[0].val.clusterDim.x = 1;
-                at[0].val.clusterDim.y = 1;
-                at[0].val.clusterDim.z = 1 << ls;
-                q.attrs = at;
-                q.numAttrs = 1;
-                e = cudaOccupancyMaxActiveClusters(&n[ls], kern, &q);
+                e = clusters_at_once(kern, max_warps(MV) * 32, kBlockSmem, 1, 1 << ls, &n[ls]);
                 if (e != cudaSuccess) return e;
             }
             std::copy(n, n + 4, v);
