@@ -117,10 +117,11 @@ __host__ __device__ constexpr int columns_of(int mv) { return 2 * mv; }
 __host__ __device__ constexpr int act_group_bytes(int mv) { return 4 * columns_of(mv) * 64; }
 // Whether a warp's sums take the place of its first group's activations, which are
 // in registers by then.  It brings gate/up of four vectors at 2560 x 9728 to one
-// block an SM (12.7 us against 17.9); elsewhere room is left or nothing is gained,
+// block an SM (10.2 us against 14.8); elsewhere room is left or nothing is gained,
 // and a place of their own is 2 to 9 % faster.
 __host__ __device__ constexpr bool sums_in_act(int mv, int parts) { return mv == 4 && parts == 2; }
-__host__ __device__ constexpr int max_warps(int mv) { return mv >= 4 ? 16 : 20; }
+// (20 at eight vectors, in 96 registers, took 8.6 us instead of 8.2 on 8208 x 2560.)
+__host__ __device__ constexpr int max_warps(int mv) { return mv == 8 ? 16 : 20; }
 __host__ __device__ inline int row_pitch(int share) { return share * 64 + (share & 1 ? 0 : 64); }
 struct W4Smem {
     uint32_t act, par, scales, sums, sq, tot, total;
@@ -148,7 +149,13 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
     const int r = lane >> 2, t = lane & 3;
     const int groups = p.K / kW4Group, rank = blockIdx.z, split = 1 << c.log_split;
     const int k0 = groups * rank >> c.log_split, kg = (groups * (rank + 1) >> c.log_split) - k0;  // this block's groups of K
-    const int g0 = (int)(kg * warp * c.magic >> 32), g1 = (int)(kg * (warp + 1) * c.magic >> 32);  // this warp's of those
+    // this warp's of those; where they do not come out even, the last warps have one
+    // more: they copy no rows, and neighbours are on different schedulers (8208 x 2560 at
+    // eight vectors, 20 groups for 16 warps: 8.2 us; 10.1 with every fourth warp, all of
+    // one scheduler, having two)
+    const int each = (int)(kg * c.magic >> 32), even = W - (kg - each * W);
+    auto first_of = [&](int w) { return each * w + max(w - even, 0); };
+    const int g0 = first_of(warp), g1 = first_of(warp + 1);
     const int ntiles = (p.N + 15) / 16;
     const int tile0 = blockIdx.x, step = gridDim.x;
     // this block's tiles: tile0, tile0 + step, ...
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
                 if (!kInAct) {
                     v[h] += all[(size_t)w * outs * PARTS + first + h * 16 * MV];
                 } else {  // where warp w's first group was, if it had any
-                    const int from = (int)(kg * w * c.magic >> 32), to = (int)(kg * (w + 1) * c.magic >> 32);
+                    const int from = first_of(w), to = first_of(w + 1);
                     const float* theirs = reinterpret_cast<const float*>(smem + o.act + from * act_group_bytes(MV));
                     if (from < to) v[h] += theirs[first + h * 16 * MV];
                 }
@@ -470,21 +477,8 @@ constexpr size_t kBlockSmem = 227 * 1024 - 1024;  // the barriers' share left ou
 // at_once[i]: clusters of 2^i blocks of this kernel that run at once.
 W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, const int at_once[4]) {
     const int groups = p.K / kW4Group, ntiles = (p.N + 15) / 16;
-    auto warps_for = [&](int share) {
-        // a group takes a scheduler about 90 cycles of issue and a warp about 400 from
-        // load to sum: the count with the shortest tile, ties to more warps
-        int best = 1, best_cost = 1 << 30;
-        for (int w = std::min(share, max_warps(mv)); w >= 1; --w) {
-            const int cost = (share + w - 1) / w * std::max(2 * ((w + 3) / 4), 9);
-            if (cost < best_cost) {
-                best_cost = cost;
-                best = w;
-            }
-        }
-        return best;
-    };
     auto made = [&](int log_split, int tiles, int grid) {
-        const int share = (groups + (1 << log_split) - 1) >> log_split, warps = warps_for(share);
+        const int share = (groups + (1 << log_split) - 1) >> log_split, warps = std::min(share, max_warps(mv));
         return W4Launch{warps, tiles, share, log_split, grid, ((1ull << 32) + warps - 1) / warps,
                         smem_of(mv, parts, tiles, share, warps).total};
     };
@@ -492,7 +486,7 @@ W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, const int at_once[4]
     // least: a warp's turns (groups of K, between the most a warp has and the mean)
     // times its tiles and the preparation of its vectors, and 2.2 tiles for joining
     // a cluster.  2560 x 9728 at 1, 2, 4 vectors: K in four 7.7, 7.7, 7.9 us, the least
-    // split that fits 8.0, 8.7, 9.2; 2560 x 4096: K whole 4.7, 5.0, 5.4 against 5.4, 5.4, 5.7
+    // split that fits 8.0, 8.7, 9.2; 2560 x 4096: K whole 4.6, 4.9, 5.4 against 5.4, 5.4, 5.7
     // in two, at 8 vectors 7.8 against 7.1.  (Clusters of 3, 5 and 6 blocks were
     // slower than of 4 and 8 throughout.)
     W4Launch best{};
