@@ -30,6 +30,10 @@ constexpr int kRun = 32 * kRunNv;
 // frames x 8 x 1026, 5 alternatives: 29.7 us; 8 rows 30.1, 16 rows 33.5).
 constexpr int kShortWarps = 4;
 constexpr int kLongWarps = 16;            // warps a block, at most, long rows
+// Up to so many alternatives the lanes' maxima are taken one by one to find the
+// bound, above it by halving (4096 frames x 8 x 1026: 8 alternatives 32.0 us one by
+// one, 30.9 by halving; 3 28.4 and 29.5).
+constexpr int kOneByOne = 5;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -124,7 +128,7 @@ __device__ __forceinline__ void sort_candidates(Candidates& c, int n, int top, f
 // that fails (ties across the bound), with a NaN in the run, or where fewer than
 // `top` lanes have an entry above -inf, they are taken out one by one instead.
 // (One by one throughout took 41 us on 4096 frames x 8 x 1026 with 5 alternatives
-// and 158 us with 32; now 30 and 64, and 22 without alternatives.)
+// and 158 us with 32; now 29.5 and 48, and 22 without alternatives.)
 template <int NV, bool LISTED>  // LISTED: it comes with a list
 __device__ __forceinline__ Part warp_run(const float* z, int n, int first, float c, int top, Candidates& cand,
                                          float& list_v, int& list_i) {
@@ -187,10 +191,27 @@ __device__ __forceinline__ Part warp_run(const float* z, int n, int first, float
     uint32_t low = 0;
     {
         uint32_t key = ranked(fmaxf(m, old_v));
-        for (int k = 0; k < top; ++k) {
-            low = __reduce_max_sync(kAll, key);
-            if (low <= kRankedNone) break;
-            if (lane == __ffs(__ballot_sync(kAll, key == low)) - 1) key = 0;
+        if (top <= kOneByOne) {
+            for (int k = 0; k < top; ++k) {
+                low = __reduce_max_sync(kAll, key);
+                if (low <= kRankedNone) break;
+                if (lane == __ffs(__ballot_sync(kAll, key == low)) - 1) key = 0;
+            }
+        } else {  // or a lower one that no more lanes reach, by halving
+            uint32_t high = (LISTED ? __reduce_max_sync(kAll, key) : ranked(r.m)) + 1u;
+            low = max(__reduce_min_sync(kAll, key), kRankedNone + 1u);
+            int reach = __popc(__ballot_sync(kAll, key >= low));
+            if (reach < top) low = 0;
+            while (reach > top && low + 1u < high) {
+                const uint32_t mid = low + (high - low) / 2u;
+                const int n = __popc(__ballot_sync(kAll, key >= mid));
+                if (n >= top) {
+                    low = mid;
+                    reach = n;
+                } else {
+                    high = mid;
+                }
+            }
         }
     }
     if (low > kRankedNone && !r.nan) {
@@ -377,14 +398,15 @@ __global__ void __launch_bounds__(kShortWarps * 32) logprobs_short_kernel(const 
 }
 
 // A cluster of gridDim.y blocks a row: its warps take runs of the row in turn.
-__global__ void __launch_bounds__(kLongWarps * 32) logprobs_long_kernel(const LogprobParams p) {
+__global__ void __launch_bounds__(kLongWarps * 32, 2) logprobs_long_kernel(const LogprobParams p) {
     __shared__ Part parts[kLongWarps];
-    __shared__ Candidates lists[kLongWarps];  // a warp's gathered entries, then its list
-    // what the cluster's blocks hand to its first
+    // a warp's gathered entries, then its list; and in a cluster the blocks' lists,
+    // which they hand to the first
+    extern __shared__ Candidates lists[];
     __shared__ Part block_part[8];
-    __shared__ Candidates block_list[8];
     namespace cg = cooperative_groups;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, W = blockDim.x >> 5, C = gridDim.y;
+    Candidates* block_list = lists + W;
     if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // all blocks run: awaited below
     pdl_trigger();
     pdl_wait();
@@ -431,12 +453,25 @@ cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t s) {
         return launch_ordered(p.V <= 256 ? logprobs_short_kernel<8> : logprobs_short_kernel<kRunNv>, dim3(grid),
                               dim3(kShortWarps * 32), 0, s, 1, 1, p, items);
     }
-    const int runs = (p.V + kRun - 1) / kRun, W = std::min(kLongWarps, runs);
+    // Warps a row, each with its runs in turn: the least rounds of blocks (32 warps
+    // an SM) times turns, and of equals the fewest, four at least, as there are fewer
+    // lists to merge and few entries of a later run are above a warp's list.  (20
+    // alternatives: 512 x 32000 8 warps 25.3 us, 11 warps 30.4, 16 warps 28.6;
+    // 2000 x 8192 4 warps 26.4, 2 warps 27.8, 8 warps 32.9.)
+    const int runs = (p.V + kRun - 1) / kRun;
+    int W = std::min(kLongWarps, runs);
+    const auto cost = [&](int w) {
+        const long long at_once = 152 * (32 / w);
+        return (items + at_once - 1) / at_once * ((runs + w - 1) / w);
+    };
+    for (int w = W - 1; w >= 4; --w)
+        if (cost(w) <= cost(W)) W = w;
     // one block a row, or so many that every warp has one run, while the rows do
     // not fill the SMs by themselves
     int C = 1;
     while (C < 8 && C * W < runs && (long long)items * C < 152) C *= 2;
-    return launch_ordered(logprobs_long_kernel, dim3(items, C), dim3(W * 32), 0, s, C, 1, p);
+    const size_t smem = sizeof(Candidates) * (W + (C > 1 ? C : 0));
+    return launch_ordered(logprobs_long_kernel, dim3(items, C), dim3(W * 32), smem, s, C, 1, p);
 }
 
 }  // namespace tts

@@ -62,6 +62,19 @@ def test_code_logprobs(ads, rows, n_cb, V, top, T, pad):
     assert all(np.array_equal(a, b, equal_nan=True) for a, b in zip(got, again))
 
 
+@pytest.mark.parametrize("rows,n_cb,V,top", [(2000, 1, 5300, 20), (600, 1, 17000, 6), (330, 2, 3200, 32), (700, 1, 9000, 1)])
+def test_many_long_rows(ads, rows, n_cb, V, top):
+    """Rows enough for a warp to take several runs of each: runs that rise, so that
+    the alternatives found first are replaced, that fall, and ones of a few values,
+    where most entries are equal."""
+    z = synth.normal_f32(7, V + top, (rows, n_cb, V), std=2.0)
+    z[0::4] += np.linspace(-6.0, 6.0, V, dtype=np.float32)
+    z[1::4] -= np.linspace(-6.0, 6.0, V, dtype=np.float32)
+    z[2::4] = np.round(z[2::4])
+    codes = codes_for(rows, n_cb, V, V)
+    check(run(ads, z, codes, top), z, codes, top)
+
+
 @pytest.mark.parametrize("V", [5, 1026, 9001])
 def test_ties_go_to_the_lowest_code(ads, V):
     z = np.round(synth.normal_f32(7, 3, (6, 2, V)) * 2).astype(np.float32)
