@@ -495,9 +495,11 @@ W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, const int at_once[4]
     // split that fits 8.0, 8.7, 9.2; 2560 x 4096: K whole 4.6, 4.9, 5.4 against 5.4, 5.4, 5.7
     // in two, at 8 vectors 7.8 against 7.1.  (Clusters of 3, 5 and 6 blocks were
     // slower than of 4 and 8 throughout.)
+    int end = 1;  // of the splits whose clusters the device has room for
+    while (end < 4 && (1 << end) <= groups && at_once[end] > 0) ++end;
     W4Launch best{};
     float least = 0.f;
-    for (int ls = 0; ls < 4 && (1 << ls) <= groups; ++ls) {
+    for (int ls = 0; ls < end; ++ls) {
         const int most = std::max(1, std::min(ntiles, at_once[ls])), tiles = (ntiles + most - 1) / most;
         if (tiles > (sums_in_act(mv, parts) ? kMaxTiles / 2 : kMaxTiles)) continue;
         const W4Launch c = made(ls, tiles, most);
@@ -511,10 +513,10 @@ W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, const int at_once[4]
     }
     if (best.warps) return best;
     // more tiles than that: as many a block as fit, over several rounds of blocks
-    for (int ls = 0; ls < 4 && (1 << ls) <= groups; ++ls)
+    for (int ls = 0; ls < end; ++ls)
         for (int tiles = std::min(sums_in_act(mv, parts) ? kMaxTiles / 2 : kMaxTiles, ntiles); tiles >= 1; --tiles) {
             const W4Launch c = made(ls, tiles, (ntiles + tiles - 1) / tiles);
-            if (c.smem <= kBlockSmem && (tiles >= 2 || ls == 3 || (2 << ls) > groups)) return c;
+            if (c.smem <= kBlockSmem && (tiles >= 2 || ls == end - 1)) return c;
         }
     return W4Launch{};
 }
