@@ -41,6 +41,7 @@ struct Kv4Params {
     float eps;
     int S, tiles_per_split;  // splits per kv head, tiles of 16 cached positions per split
     int cluster;             // a head's splits are a cluster, joined through shared memory
+    int halves;              // 1: a kv head's eight queries are two heads of four
     unsigned* tickets;       // [n_kv], zero between calls
     float2* part_ml;         // [n_kv][S][G] maximum, sum
     float* part_o;           // [n_kv][S][G][128]
@@ -476,7 +477,8 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
     const int g = blockIdx.x, split = blockIdx.y;
     if (p.cluster) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const bool has_new = split == p.S - 1;
-    const size_t base = (size_t)g * p.max_pos;
+    const int kv = g >> p.halves;  // its head of the cache
+    const size_t base = (size_t)kv * p.max_pos;
     const int tile_end = min((p.pos + kTilePos - 1) / kTilePos, (split + 1) * p.tiles_per_split);
 
     // the angles from the launch parameters to shared memory, an entry a warp at
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
     float4 x = {};
     uint2 gain = {};
     if (warp < G || new_k || new_v) {
-        const int vec = new_v ? p.n_q + p.n_kv + g : new_k ? p.n_q + g : g * G + warp;
+        const int vec = new_v ? p.n_q + p.n_kv + kv : new_k ? p.n_q + kv : g * G + warp;
         x = reinterpret_cast<const float4*>(p.qkv)[(size_t)vec * (kHeadDim / 4) + lane];
         gain = reinterpret_cast<const uint2*>(new_k ? p.k_norm : p.q_norm)[lane];
     }
@@ -561,19 +563,20 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
         for (int j = 0; j < 4; ++j) v[j] = round_bf16(v[j]);
         uint32_t par;
         const uint32_t code = quant_row(v, &par);
-        store_row(code, par, codes + (base + p.pos) * kRowBytes, pars + (base + p.pos) * 2, lane);
+        const bool writes = !(g & p.halves);  // one of two that share the row
+        if (writes) store_row(code, par, codes + (base + p.pos) * kRowBytes, pars + (base + p.pos) * 2, lane);
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = fmaf(bf16lo(par), (float)((code >> (4 * j)) & 15u), bf16hi(par));
         const float4 q = make_float4(v[0], v[1], v[2], v[3]);
         if (keep) keep[lane] = q;
-        if (p.kv_row) reinterpret_cast<float4*>(p.kv_row)[(size_t)at_row * (kHeadDim / 4) + lane] = q;
+        if (p.kv_row && writes) reinterpret_cast<float4*>(p.kv_row)[(size_t)at_row * (kHeadDim / 4) + lane] = q;
     };
     constexpr int kThreads = kAttnWarps * 32;
     if (new_k) {
         asm volatile("bar.arrive 1, %0;" ::"n"(kThreads) : "memory");
         float k[4];
         norm_rope_exact(x, gain, rope, p.eps, lane, k);
-        store_new(k, p.k4, p.k_par, g, nullptr);
+        store_new(k, p.k4, p.k_par, kv, nullptr);
         asm volatile("bar.sync 2, %0;" ::"n"(kThreads) : "memory");
         // the new position is a partial of its own: weight 1 at its score
 #pragma unroll
@@ -588,7 +591,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
     } else {
         if (new_v) {
             float v[4] = {x.x, x.y, x.z, x.w};
-            store_new(v, p.v4, p.v_par, p.n_kv + g, reinterpret_cast<float4*>(vnew));
+            store_new(v, p.v4, p.v_par, p.n_kv + kv, reinterpret_cast<float4*>(vnew));
         }
         asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
         if (has_new) asm volatile("bar.arrive 2, %0;" ::"n"(kThreads) : "memory");
@@ -1005,31 +1008,60 @@ __global__ void __launch_bounds__(kAttnWarps * 32, 1) attn_kv4_kernel(const __gr
 
 int max_splits(int n_kv) { return n_kv >= kMaxSplitUnits ? 1 : kMaxSplitUnits / n_kv; }
 
+// How many clusters of c blocks run at once.
+struct Room {
+    int clusters[kMaxCluster + 1];
+    // the most blocks a cluster may have for `heads` clusters to run at once
+    int most(int heads) const {
+        int c = kMaxCluster;
+        while (c > 1 && clusters[c] < heads) --c;
+        return c;
+    }
+};
+
+// Per device: the shared-memory limit raised, and the clusters there is room for (a
+// cluster stays within a group of SMs; above 8 blocks is this device's own, so it is
+// asked for).
+template <int G>
+cudaError_t prepare_attn_kv4(int dev, int sms, Room* room) {
+    static std::mutex mu;
+    static Room rooms[64] = {};
+    const auto kern = attn_kv4_kernel<G>;
+    const std::lock_guard<std::mutex> lock(mu);
+    Room& known = rooms[dev & 63];
+    if (!known.clusters[1]) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        Room r = {{0, sms}};
+        for (int c = 2; c <= kMaxCluster; ++c) {
+            e = clusters_at_once(kern, kAttnWarps * 32, kAttnSmem, c, 1, &r.clusters[c]);
+            if (e != cudaSuccess) return e;
+        }
+        known = r;
+    }
+    *room = known;
+    return cudaSuccess;
+}
+
 template <int G>
 cudaError_t launch_attn_kv4(Kv4Params p, int dev, int sms, cudaStream_t s) {
-    // per device: the shared-memory limit raised, and how many clusters of 2 .. 16
-    // blocks run at once (a cluster stays within a group of SMs; above 8 blocks is
-    // this device's own, so it is asked for)
-    static std::mutex mu;
-    static int at_once_of[64][kMaxCluster + 1] = {};
-    const auto kern = attn_kv4_kernel<G>;
-    int at_once[kMaxCluster + 1];
-    {
-        const std::lock_guard<std::mutex> lock(mu);
-        int* v = at_once_of[dev & 63];
-        if (!v[1]) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnSmem);
-            if (e != cudaSuccess) return e;
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e != cudaSuccess) return e;
-            int n[kMaxCluster + 1] = {0, sms};
-            for (int c = 2; c <= kMaxCluster; ++c) {
-                e = clusters_at_once(kern, kAttnWarps * 32, kAttnSmem, c, 1, &n[c]);
-                if (e != cudaSuccess) return e;
-            }
-            std::copy(n, n + kMaxCluster + 1, v);
+    Room room;
+    const cudaError_t e = prepare_attn_kv4<G>(dev, sms, &room);
+    if (e != cudaSuccess) return e;
+    const int tiles = (p.pos + kTilePos - 1) / kTilePos;
+    if constexpr (G == 8) {
+        // Eight queries a head as two heads of four, which read the cache twice: a tile
+        // takes a warp a sixth less time and a call 1 us less for its queries and partials
+        // (16/2 heads, 1000 positions 5.1 us against 5.9, 20000 9.8 against 11.6), while
+        // that leaves a warp one tile, or four where there are SMs for sixteen blocks a
+        // head (64/8 heads, 6000 positions 9.7 against 9.1; 32/4, 40000 16.6 against 15.0).
+        const int heads = 2 * p.n_kv, wide = sms / heads;
+        if (wide >= 1 && (tiles <= kAttnWarps * room.most(heads) || (wide >= 16 && tiles <= 4 * kAttnWarps * wide))) {
+            p.halves = 1;
+            return launch_attn_kv4<4>(p, dev, sms, s);
         }
-        std::copy(v, v + kMaxCluster + 1, at_once);
     }
     // How a head's cache is split, none empty (us a call at 32/8 heads unless said):
     // - up to 192 positions one block takes it: 4.3 at 100 against 5.0 in two
@@ -1041,21 +1073,18 @@ cudaError_t launch_attn_kv4(Kv4Params p, int dev, int sms, cudaStream_t s) {
     // - and where that leaves a warp more than two tiles, blocks all over the
     //   device, a tile a warp, joined through global memory: 8.5 at 8000
     //   positions against 8.7, but 7.8 at 5000 against 7.5.  Eight queries a head, with
-    //   partials twice as large, break even at three tiles (14000, 16/2 heads).
-    const int tiles = (p.pos + kTilePos - 1) / kTilePos;
+    //   partials twice as large, break even at three tiles.
+    const int heads = p.n_kv << p.halves;
     int S = 1;
     if (tiles > kOneBlockTiles) {
-        int most = 1;
-        for (int c = 2; c <= kMaxCluster; ++c)
-            if (at_once[c] >= p.n_kv) most = c;
-        S = std::min(most, (tiles + kClusterTiles - 1) / kClusterTiles);
+        S = std::min(room.most(heads), (tiles + kClusterTiles - 1) / kClusterTiles);
         p.cluster = S > 1 && tiles <= S * kAttnWarps * (G == 8 ? 3 : 2);
         if (!p.cluster)
-            S = std::max(1, std::min({(tiles + kAttnWarps - 1) / kAttnWarps, max_splits(p.n_kv), sms / p.n_kv}));
+            S = std::max(1, std::min({(tiles + kAttnWarps - 1) / kAttnWarps, max_splits(p.n_kv), sms / heads}));
     }
     p.tiles_per_split = std::max(1, (tiles + S - 1) / S);
     p.S = std::max(1, (tiles + p.tiles_per_split - 1) / p.tiles_per_split);
-    return launch_ordered(kern, dim3(p.n_kv, p.S), dim3(kAttnWarps * 32), kAttnSmem, s, p.cluster ? p.S : 1, 1, p);
+    return launch_ordered(attn_kv4_kernel<G>, dim3(heads, p.S), dim3(kAttnWarps * 32), kAttnSmem, s, p.cluster ? p.S : 1, 1, p);
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {

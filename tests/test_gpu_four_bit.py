@@ -362,7 +362,10 @@ def test_attention_kv4_streams_and_graphs(ads):
 # out even.
 DIVIDED = [(32, 8, 192), (32, 8, 193), (32, 8, 2047), (32, 8, 6144), (32, 8, 6145), (4, 1, 8192), (4, 1, 8193),
            (8, 1, 12288), (8, 1, 12289), (16, 2, 2900), (2, 2, 3900), (2, 2, 8300), (12, 6, 1800), (6, 3, 9100),
-           (16, 16, 1000), (33, 33, 700), (9, 9, 5000), (160, 40, 900)]
+           (16, 16, 1000), (33, 33, 700), (9, 9, 5000), (160, 40, 900),
+           # eight queries a head: two heads of four, or one of eight
+           (8, 1, 0), (24, 3, 31), (16, 2, 200), (32, 4, 9728), (32, 4, 19500), (40, 5, 2000), (40, 5, 4100),
+           (128, 16, 900), (128, 16, 1800), (800, 100, 70)]
 
 
 @pytest.mark.parametrize("n_q,n_kv,pos", DIVIDED)
