@@ -41,7 +41,7 @@ struct Kv4Params {
     float eps;
     int S, tiles_per_split;  // splits per kv head, tiles of 16 cached positions per split
     int cluster;             // a head's splits are a cluster, joined through shared memory
-    int halves;              // 1: a kv head's eight queries are two heads of four
+    int halves;              // 1: a kv head's queries are two heads
     unsigned* tickets;       // [n_kv], zero between calls
     float2* part_ml;         // [n_kv][S][G] maximum, sum
     float* part_o;           // [n_kv][S][G][128]
@@ -1051,19 +1051,24 @@ cudaError_t launch_attn_kv4(Kv4Params p, int dev, int sms, cudaStream_t s) {
     const cudaError_t e = prepare_attn_kv4<G>(dev, sms, &room);
     if (e != cudaSuccess) return e;
     const int tiles = (p.pos + kTilePos - 1) / kTilePos;
-    if constexpr (G == 8) {
-        // Eight queries a head as two heads of four, which read the cache twice: a tile
-        // takes a warp a sixth less time and a call 1 us less for its queries and partials
-        // (16/2 heads, 1000 positions 5.1 us against 5.9, 20000 9.8 against 11.6), while
-        // that leaves a warp one tile, or four where there are SMs for sixteen blocks a
-        // head (64/8 heads, 6000 positions 9.7 against 9.1; 32/4, 40000 16.6 against 15.0).
-        const int heads = 2 * p.n_kv, wide = sms / heads;
-        if (wide >= 1 && (tiles <= kAttnWarps * room.most(heads) || (wide >= 16 && tiles <= 4 * kAttnWarps * wide))) {
+    if constexpr (G >= 4) {
+        // The queries of a head as two heads, which read the cache twice, while SMs are
+        // left.  Eight as four and four: a tile takes a warp a sixth less time and a
+        // call 1 us less for its queries and partials (16/2 heads, 1000 positions 5.1 us
+        // against 5.9, 20000 9.8 against 11.6), while that leaves a warp one tile, or
+        // four where there are SMs for sixteen blocks a head (64/8 heads, 6000
+        // positions 9.7 against 9.1; 32/4, 40000 16.6 against 15.0).  Four as two and two
+        // save 0.3 us while half the warps have a tile (32/8 heads, position 0 3.7 against
+        // 4.0, 700 5.1 against 5.6, but 1279 5.8 against 5.5).
+        const int heads = 2 * p.n_kv, wide = sms / heads, turn = kAttnWarps * room.most(heads);
+        const bool two = G == 8 ? tiles <= turn || (wide >= 16 && tiles <= 4 * kAttnWarps * wide) : tiles <= turn / 2;
+        if (two && wide >= 1 && !p.halves) {
             p.halves = 1;
-            return launch_attn_kv4<4>(p, dev, sms, s);
+            return launch_attn_kv4<G / 2>(p, dev, sms, s);
         }
     }
-    // How a head's cache is split, none empty (us a call at 32/8 heads unless said):
+    // How a head's cache is split, none empty (us a call at 32/8 heads, none of
+    // them as two):
     // - up to 192 positions one block takes it: 4.3 at 100 against 5.0 in two
     //   blocks, 5.05 at 200 against 4.9 in four;
     // - then a cluster, whose blocks join through shared memory, four tiles a
