@@ -481,16 +481,16 @@ extern "C" int tts_code_logprobs(const float* logits, long long ld, const int32_
                                  int32_t* top_codes, float* top_logprob, void* stream) {
     using namespace tts;
     if (rows < 0 || n_cb < 1 || n_cb > kMaxCodebooks || cb_vocab < 2 || cb_vocab > (1 << 20)) return TTS_ERR_ARG;
-    if (!logits || ld < (long long)n_cb * cb_vocab || top < 0 || top > kMaxTop || top > cb_vocab) return TTS_ERR_ARG;
+    if (ld < (long long)n_cb * cb_vocab || top < 0 || top > kMaxTop || top > cb_vocab) return TTS_ERR_ARG;
     if ((long long)rows * n_cb > 0x7fffffffLL - kShortWarps) return TTS_ERR_ARG;
     if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(kLog2e / temperature)) return TTS_ERR_ARG;
-    if ((logprob != nullptr) != (codes != nullptr)) return TTS_ERR_ARG;
+    if (rows == 0) return TTS_OK;  // an empty array may have no address
+    if (!logits || (logprob != nullptr) != (codes != nullptr)) return TTS_ERR_ARG;
     if ((top > 0) != (top_codes != nullptr) || (top > 0) != (top_logprob != nullptr)) return TTS_ERR_ARG;
     const uintptr_t all = reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(codes) |
                           reinterpret_cast<uintptr_t>(logprob) | reinterpret_cast<uintptr_t>(entropy) |
                           reinterpret_cast<uintptr_t>(top_codes) | reinterpret_cast<uintptr_t>(top_logprob);
     if (all & 3) return TTS_ERR_ARG;
-    if (rows == 0) return TTS_OK;
     LogprobParams p{logits, ld, codes, rows, n_cb, cb_vocab, 1.f / temperature, top, logprob, entropy, top_codes,
                     top_logprob};
     const cudaError_t e = launch_logprobs(p, static_cast<cudaStream_t>(stream));

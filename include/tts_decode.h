@@ -476,8 +476,9 @@ int tts_attention_decode_kv4(const float* qkv, const void* q_norm, const void* k
  * codebook with nothing but -inf has log probabilities -inf and entropy 0.
  * With a NaN or +inf among its logits a codebook's log probabilities and
  * entropy are NaN; NaN entries rank last.  DEVICE outputs, fp32 and int32.
- * 0 <= rows, 1 <= n_cb <= 8, 2 <= cb_vocab <= 2^20, 0 <= top <= min(32,
- * cb_vocab), temperature positive and finite.  Pointers 4-byte aligned.
+ * 0 <= rows (0: nothing is done, pointers may be NULL), 1 <= n_cb <= 8,
+ * 2 <= cb_vocab <= 2^20, 0 <= top <= min(32, cb_vocab), temperature positive
+ * and finite.  Pointers 4-byte aligned.
  * Enqueued on `stream` (NULL: the default stream); does not synchronise; may
  * be captured.  TTS_ERR_ARG otherwise. */
 int tts_code_logprobs(const float* logits, long long ld, const int32_t* codes, int rows, int n_cb, int cb_vocab,
