@@ -204,13 +204,25 @@ def attention_decode(qkv, q_norm, k_norm, k_cache, v_cache, out, n_q: int, n_kv:
 # 4-bit weights, 4-bit cache, scores of codes
 # ----------------------------------------------------------------------------
 
-def _check(fn: str, *wanted):
-    """Each of `wanted` is (tensor or None, bytes): raises TtsError(TTS_ERR_ARG)
-    unless the tensor is a contiguous CUDA tensor of that many bytes (its address
-    and size are all the library sees)."""
-    for t, n in wanted:
-        if t is not None and (t.nbytes != n or not t.is_cuda or not t.is_contiguous()):
-            raise TtsError(fn, -1)
+# The library sees an address of each tensor and nothing else, so the binding
+# checks that a tensor is of its element type and size, contiguous, and on the
+# current device like the others.  The checks are written out: they are host time
+# of every launch, and by a loop over (tensor, type, size) attention_decode_kv4's
+# ten tensors took 1.6 us more (9.6 us a call against 8.0).
+_types = None  # fp32, int32, uint8, bf16 (or its bits), whether there are several devices
+
+
+def _get_types():
+    global _types
+    torch = _torch()
+    _types = (torch.float32, torch.int32, torch.uint8, (torch.bfloat16, torch.int16, torch.uint16),
+              torch.cuda.device_count() > 1)
+    return _types
+
+
+def _elsewhere(dev: int, several: bool) -> bool:
+    """Whether device number dev (below 0: the host) is not the current one."""
+    return dev < 0 or (several and dev != _torch().cuda.current_device())
 
 
 def _opt(t):
@@ -221,8 +233,10 @@ def quantize_w4_weight(w_dev, stream=None):
     """tts_quantize_w4_weight on w_dev, bf16 (or int16 bf16 bits) [N][K]:
     returns (uint8 [N][K/2], bfloat16 [N][K/128]) device tensors."""
     torch = _torch()
+    bf16, several = (_types or _get_types())[3:]
     N, K = w_dev.shape
-    _check("tts_quantize_w4_weight", (w_dev, 2 * N * K))
+    if w_dev.dtype not in bf16 or not w_dev.is_contiguous() or _elsewhere(w_dev.get_device(), several):
+        raise TtsError("tts_quantize_w4_weight", -1)
     q = torch.empty((N, K // 2), dtype=torch.uint8, device=w_dev.device)
     s = torch.empty((N, K // 128), dtype=torch.bfloat16, device=w_dev.device)
     _call("tts_quantize_w4_weight", w_dev.data_ptr(), N, K, q.data_ptr(), s.data_ptr(), stream)
@@ -235,29 +249,62 @@ def gemv_w4(x_dev, w4_dev, s_dev, y_dev, epi: int = 0, resid_dev=None, gamma_dev
     [N][K/128] (epi 2: 2N rows, gate then up), y_dev fp32 [M][N]; resid_dev
     fp32 [M][N] for epi 1 (y_dev itself to add in place); gamma_dev bf16 [K]
     normalises x."""
+    f32, _, u8, bf16, several = _types or _get_types()
     M, K = x_dev.shape
     N = y_dev.shape[-1]
     rows = 2 * N if epi == 2 else N
-    _check("tts_gemv_w4", (x_dev, 4 * M * K), (w4_dev, rows * (K // 2)), (s_dev, 2 * rows * (K // 128)),
-           (y_dev, 4 * M * N), (resid_dev, 4 * M * N), (gamma_dev, 2 * K))
+    dev = x_dev.get_device()
+    if (x_dev.dtype is not f32 or not x_dev.is_contiguous()
+            or w4_dev.dtype is not u8 or w4_dev.numel() != rows * (K // 2)
+            or w4_dev.get_device() != dev or not w4_dev.is_contiguous()
+            or s_dev.dtype not in bf16 or s_dev.numel() != rows * (K // 128)
+            or s_dev.get_device() != dev or not s_dev.is_contiguous()
+            or y_dev.dtype is not f32 or y_dev.numel() != M * N
+            or y_dev.get_device() != dev or not y_dev.is_contiguous()
+            or resid_dev is not None and (resid_dev.dtype is not f32 or resid_dev.numel() != M * N
+                                          or resid_dev.get_device() != dev or not resid_dev.is_contiguous())
+            or gamma_dev is not None and (gamma_dev.dtype not in bf16 or gamma_dev.numel() != K
+                                          or gamma_dev.get_device() != dev or not gamma_dev.is_contiguous())
+            or _elsewhere(dev, several)):
+        raise TtsError("tts_gemv_w4", -1)
     _call("tts_gemv_w4", x_dev.data_ptr(), w4_dev.data_ptr(), s_dev.data_ptr(), _opt(resid_dev), _opt(gamma_dev),
           y_dev.data_ptr(), M, N, K, epi, eps, stream)
 
 
-def _check_kv4(fn: str, k4, v4, k_par, v_par):
-    n_kv, max_pos, _ = k4.shape
-    rows = n_kv * max_pos
-    _check(fn, (k4, rows * 64), (v4, rows * 64), (k_par, 2 * rows * 4), (v_par, 2 * rows * 4))
-    return n_kv, max_pos
+def _kv4_cache(fn: str, k4, v4, k_par, v_par):
+    """The heads, positions a head and device of a 4-bit cache's tensors, checked."""
+    _, _, u8, bf16, several = _types or _get_types()
+    n_kv, max_pos, row = k4.shape
+    n = n_kv * max_pos
+    dev = k4.get_device()
+    if (row != 64 or k4.dtype is not u8 or not k4.is_contiguous()
+            or v4.dtype is not u8 or v4.numel() != n * 64 or v4.get_device() != dev or not v4.is_contiguous()
+            or k_par.dtype not in bf16 or k_par.numel() != n * 4
+            or k_par.get_device() != dev or not k_par.is_contiguous()
+            or v_par.dtype not in bf16 or v_par.numel() != n * 4
+            or v_par.get_device() != dev or not v_par.is_contiguous() or _elsewhere(dev, several)):
+        raise TtsError(fn, -1)
+    return n_kv, max_pos, dev
+
+
+def _bf16_rows(fn: str, k_dev, v_dev, n_kv: int, dev: int) -> int:
+    """The positions a head of bf16 caches [n_kv][positions][128], checked."""
+    bf16 = _types[3]
+    stride = k_dev.shape[1]
+    n = n_kv * stride * 128
+    if (k_dev.dtype not in bf16 or k_dev.numel() != n or k_dev.get_device() != dev or not k_dev.is_contiguous()
+            or v_dev.dtype not in bf16 or v_dev.numel() != n or v_dev.get_device() != dev
+            or not v_dev.is_contiguous()):
+        raise TtsError(fn, -1)
+    return stride
 
 
 def quantize_kv4(k_dev, v_dev, k4, v4, k_par, v_par, p0: int, p1: int, stream=None) -> None:
     """tts_quantize_kv4: positions [p0, p1) of bf16 caches [n_kv][stride][128]
     into the 4-bit cache: k4, v4 uint8 [n_kv][max_pos][64], k_par, v_par bf16
     [n_kv][max_pos][2][2]."""
-    n_kv, max_pos = _check_kv4("tts_quantize_kv4", k4, v4, k_par, v_par)
-    stride = k_dev.shape[1]
-    _check("tts_quantize_kv4", (k_dev, 2 * n_kv * stride * 128), (v_dev, 2 * n_kv * stride * 128))
+    n_kv, max_pos, dev = _kv4_cache("tts_quantize_kv4", k4, v4, k_par, v_par)
+    stride = _bf16_rows("tts_quantize_kv4", k_dev, v_dev, n_kv, dev)
     _call("tts_quantize_kv4", k_dev.data_ptr(), v_dev.data_ptr(), n_kv, p0, p1, stride, k4.data_ptr(), v4.data_ptr(),
           k_par.data_ptr(), v_par.data_ptr(), max_pos, stream)
 
@@ -265,9 +312,8 @@ def quantize_kv4(k_dev, v_dev, k4, v4, k_par, v_par, p0: int, p1: int, stream=No
 def dequantize_kv4(k4, v4, k_par, v_par, k_dev, v_dev, p0: int, p1: int, stream=None) -> None:
     """tts_dequantize_kv4: the values of positions [p0, p1) of a 4-bit cache into
     bf16 caches [n_kv][stride][128]."""
-    n_kv, max_pos = _check_kv4("tts_dequantize_kv4", k4, v4, k_par, v_par)
-    stride = k_dev.shape[1]
-    _check("tts_dequantize_kv4", (k_dev, 2 * n_kv * stride * 128), (v_dev, 2 * n_kv * stride * 128))
+    n_kv, max_pos, dev = _kv4_cache("tts_dequantize_kv4", k4, v4, k_par, v_par)
+    stride = _bf16_rows("tts_dequantize_kv4", k_dev, v_dev, n_kv, dev)
     _call("tts_dequantize_kv4", k4.data_ptr(), v4.data_ptr(), k_par.data_ptr(), v_par.data_ptr(), n_kv, p0, p1,
           max_pos, k_dev.data_ptr(), v_dev.data_ptr(), stride, stream)
 
@@ -287,26 +333,37 @@ def attention_decode_kv4(qkv, q_norm, k_norm, k4, v4, k_par, v_par, out, n_q: in
     takes it, out fp32 [n_q 128], workspace a uint8 tensor of
     kv4_workspace_bytes zeros (kept between calls), kv_row fp32 [2][n_kv][128]
     or None."""
-    heads, max_pos = _check_kv4("tts_attention_decode_kv4", k4, v4, k_par, v_par)
-    ws_bytes = workspace.numel()
-    _check("tts_attention_decode_kv4", (qkv, 4 * (n_q + 2 * n_kv) * 128), (q_norm, 2 * 128), (k_norm, 2 * 128),
-           (out, 4 * n_q * 128), (kv_row, 4 * 2 * n_kv * 128), (workspace, ws_bytes))
-    if heads != n_kv:
+    heads, max_pos, dev = _kv4_cache("tts_attention_decode_kv4", k4, v4, k_par, v_par)
+    f32, _, u8, bf16, _ = _types
+    if (heads != n_kv
+            or qkv.dtype is not f32 or qkv.numel() != (n_q + 2 * n_kv) * 128
+            or qkv.get_device() != dev or not qkv.is_contiguous()
+            or q_norm.dtype not in bf16 or q_norm.numel() != 128
+            or q_norm.get_device() != dev or not q_norm.is_contiguous()
+            or k_norm.dtype not in bf16 or k_norm.numel() != 128
+            or k_norm.get_device() != dev or not k_norm.is_contiguous()
+            or out.dtype is not f32 or out.numel() != n_q * 128
+            or out.get_device() != dev or not out.is_contiguous()
+            or kv_row is not None and (kv_row.dtype is not f32 or kv_row.numel() != 2 * n_kv * 128
+                                       or kv_row.get_device() != dev or not kv_row.is_contiguous())
+            or workspace.dtype is not u8 or workspace.get_device() != dev or not workspace.is_contiguous()):
         raise TtsError("tts_attention_decode_kv4", -1)
     _call("tts_attention_decode_kv4", qkv.data_ptr(), q_norm.data_ptr(), k_norm.data_ptr(), k4.data_ptr(),
           v4.data_ptr(), k_par.data_ptr(), v_par.data_ptr(), out.data_ptr(), _opt(kv_row), n_q, n_kv, max_pos, pos,
-          eps, rope_theta, workspace.data_ptr(), ws_bytes, stream)
+          eps, rope_theta, workspace.data_ptr(), workspace.numel(), stream)
 
 
 def code_logprobs(logits, codes, cb_vocab: int, top: int = 0, temperature: float = 1.0, stream=None):
     """tts_code_logprobs: logits fp32 [rows][ld] (rows may be strided) and codes
     int32 [rows][n_cb]; returns (logprob [rows][n_cb], entropy [rows][n_cb],
     top_codes [rows][n_cb][top], top_logprob [rows][n_cb][top])."""
-    torch = _torch()
+    f32, i32, _, _, several = _types or _get_types()
     rows, n_cb = codes.shape
-    _check("tts_code_logprobs", (codes, 4 * rows * n_cb))
-    if not (logits.is_cuda and logits.dtype is torch.float32 and logits.dim() == 2 and logits.shape[0] == rows
-            and logits.shape[1] >= n_cb * cb_vocab and logits.stride(1) == 1):
+    dev = codes.get_device()
+    if (codes.dtype is not i32 or not codes.is_contiguous()
+            or logits.dtype is not f32 or logits.get_device() != dev or logits.dim() != 2
+            or logits.shape[0] != rows or logits.shape[1] < n_cb * cb_vocab or logits.stride(1) != 1
+            or _elsewhere(dev, several)):
         raise TtsError("tts_code_logprobs", -1)
     ld = logits.stride(0) if rows > 1 else logits.shape[1]
     lp, ent = logits.new_empty((rows, n_cb)), logits.new_empty((rows, n_cb))

@@ -26,3 +26,92 @@ def test_code_logprobs_of_no_rows_wants_no_memory(lib):
     assert lib.tts_code_logprobs(*dict(none, top=0).values()) == 0
     for bad in (dict(V=1), dict(n_cb=9), dict(top=33), dict(T=0.0), dict(ld=8207)):
         assert lib.tts_code_logprobs(*dict(none, **bad).values()) == ARG, bad
+
+
+# ---- what the binding checks, on host tensors that claim a device ---------------------
+
+class On:
+    """A host tensor that says it is on a device (its address reaches no library here)."""
+
+    def __init__(self, t, device=0):
+        self.t, self.device_number = t, device
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def get_device(self):
+        return self.device_number
+
+    @property
+    def is_cuda(self):
+        return self.device_number >= 0
+
+
+def calls():
+    """Per function: its arguments, and the names of those that are tensors."""
+    import torch
+    f = lambda *s: torch.zeros(s)
+    b = lambda *s: torch.zeros(s, dtype=torch.bfloat16)
+    u = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    cache = lambda: dict(k4=u(2, 9, 64), v4=u(2, 9, 64), k_par=b(2, 9, 2, 2), v_par=b(2, 9, 2, 2))
+    return {
+        "quantize_w4_weight": dict(w_dev=b(4, 256)),
+        "gemv_w4": dict(x_dev=f(3, 256), w4_dev=u(10, 128), s_dev=b(10, 2), y_dev=f(3, 5), epi=2, gamma_dev=b(256)),
+        "gemv_w4 ": dict(x_dev=f(3, 256), w4_dev=u(5, 128), s_dev=b(5, 2), y_dev=f(3, 5), epi=1, resid_dev=f(3, 5)),
+        "quantize_kv4": dict(k_dev=b(2, 6, 128), v_dev=b(2, 6, 128), **cache(), p0=1, p1=4),
+        "dequantize_kv4": dict(**cache(), k_dev=b(2, 6, 128), v_dev=b(2, 6, 128), p0=1, p1=4),
+        "attention_decode_kv4": dict(qkv=f(8 * 128), q_norm=b(128), k_norm=b(128), **cache(), out=f(4 * 128), n_q=4,
+                                     n_kv=2, pos=3, workspace=u(64), kv_row=f(2, 2, 128)),
+        "code_logprobs": dict(logits=f(3, 40), codes=torch.zeros((3, 4), dtype=torch.int32), cb_vocab=10, top=2),
+    }
+
+
+@pytest.fixture
+def binding(lib, monkeypatch):
+    """The binding on a machine of two devices, device 0 current; what reaches the library is listed."""
+    import torch
+    import ar_decode_step_gb300 as m
+    seen = []
+    monkeypatch.setattr(m, "_call", lambda name, *args: seen.append(name))
+    monkeypatch.setattr(m, "_types", None, raising=False)
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    return m, seen
+
+
+@pytest.mark.parametrize("name", list(calls()))
+def test_binding_checks_every_tensor(binding, name):
+    """Another element type, size, layout or device of any one tensor is refused
+    before the library is called; bf16 tensors may be their bits."""
+    import torch
+    m, seen = binding
+    f = getattr(m, name.strip())
+    good = calls()[name]
+    tensors = [n for n, v in good.items() if isinstance(v, torch.Tensor)]
+
+    def call(**change):
+        args = {n: On(v) if isinstance(v, torch.Tensor) else v for n, v in good.items()}
+        args.update(change)
+        f(**args)
+
+    call()
+    call(**{n: On(good[n].view(torch.int16)) for n in tensors if good[n].dtype is torch.bfloat16})
+    assert len(seen) == 2
+    for n in tensors:
+        t = good[n]
+        shorter = t[:-1] if t.dim() == 1 or n == "codes" else t[..., :-1].contiguous()
+        bad = dict(fp16=On(t.to(torch.float16)), wider=On(t.to(torch.float64)), host=On(t, -1), elsewhere=On(t, 1))
+        bad["layout"] = On(torch.stack((t, t), -1)[..., 0])
+        if t.dtype is torch.int32:
+            bad["fp32"] = On(t.view(torch.float32))
+        if t.dtype is torch.float32:
+            bad["int32"] = On(t.view(torch.int32))
+        if n not in ("w_dev", "workspace"):  # their sizes are the library's to check
+            bad["size"] = On(shorter)
+        for kind, wrong in bad.items():
+            with pytest.raises(m.TtsError) as e:
+                call(**{n: wrong})
+            assert e.value.status == ARG, (n, kind)
+    with pytest.raises(m.TtsError):  # all on one device, but not the current one
+        call(**{n: On(good[n], 1) for n in tensors})
+    assert len(seen) == 2

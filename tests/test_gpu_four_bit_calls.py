@@ -28,3 +28,25 @@ def test_code_logprobs_of_an_empty_batch(ads, V, top):
                                            torch.empty((0, 2), dtype=torch.int32, device="cuda"), V, top=top)
     assert lp.shape == ent.shape == (0, 2) and at.shape == at_lp.shape == (0, 2, top)
     assert at.dtype == torch.int32 and lp.dtype == torch.float32
+
+
+def test_tensors_of_another_type_size_or_layout_are_refused(ads):
+    """One change each, on tensors of the GPU that is used; nothing is launched."""
+    import torch
+    x, w4 = torch.randn((2, 256), device="cuda"), torch.zeros((6, 128), dtype=torch.uint8, device="cuda")
+    s, y = torch.ones((6, 2), dtype=torch.bfloat16, device="cuda"), torch.full((2, 6), 7.0, device="cuda")
+    z, codes = torch.randn((3, 40), device="cuda"), torch.zeros((3, 4), dtype=torch.int32, device="cuda")
+    gamma = torch.ones(256, dtype=torch.float16, device="cuda")
+    bad = [lambda: ads.gemv_w4(x.half(), w4, s, y), lambda: ads.gemv_w4(x, w4, s.half(), y),
+           lambda: ads.gemv_w4(x, w4, s, y, gamma_dev=gamma), lambda: ads.gemv_w4(x, w4[:5], s, y),
+           lambda: ads.gemv_w4(x.t().contiguous().t(), w4, s, y), lambda: ads.gemv_w4(x, w4, s, y.cpu()),
+           lambda: ads.code_logprobs(z, codes.float(), 10), lambda: ads.code_logprobs(z, codes.t().contiguous().t(), 10),
+           lambda: ads.code_logprobs(z[:2], codes, 10), lambda: ads.code_logprobs(z[:, ::2], codes[:, :2].contiguous(), 10),
+           lambda: ads.quantize_w4_weight(torch.zeros((4, 256), dtype=torch.float16, device="cuda"))]
+    for call in bad:
+        with pytest.raises(ads.TtsError) as e:
+            call()
+        assert e.value.status == -1
+    assert (y == 7.0).all()
+    ads.gemv_w4(x, w4, s, y)
+    assert ads.code_logprobs(z, codes, 10, top=2)[2].dtype == torch.int32
