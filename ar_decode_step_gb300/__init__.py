@@ -225,20 +225,34 @@ def _elsewhere(dev: int, several: bool) -> bool:
     return dev < 0 or (several and dev != _torch().cuda.current_device())
 
 
+def _fresh(stream, dev: int, make):
+    """make()'s new tensors, allocated for `stream` (None: the default stream) on
+    device number dev.  The allocator reuses memory in the order of the stream it was
+    asked on: results of torch's current stream, written on another, could still be
+    in use by what ran before on the current one."""
+    torch = _torch()
+    if torch._C._cuda_getCurrentRawStream(dev) == (stream or 0):  # (current_stream() takes 3 us)
+        return make()
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)):
+        return make()
+
+
 def _opt(t):
     return None if t is None else t.data_ptr()
 
 
 def quantize_w4_weight(w_dev, stream=None):
     """tts_quantize_w4_weight on w_dev, bf16 (or int16 bf16 bits) [N][K]:
-    returns (uint8 [N][K/2], bfloat16 [N][K/128]) device tensors."""
-    torch = _torch()
-    bf16, several = (_types or _get_types())[3:]
+    returns (uint8 [N][K/2], bfloat16 [N][K/128]) device tensors, made for
+    `stream` (None: the default stream, whatever torch's current one is)."""
+    _, _, u8, bf16, several = _types or _get_types()
     N, K = w_dev.shape
-    if w_dev.dtype not in bf16 or not w_dev.is_contiguous() or _elsewhere(w_dev.get_device(), several):
+    dev = w_dev.get_device()
+    if w_dev.dtype not in bf16 or not w_dev.is_contiguous() or _elsewhere(dev, several):
         raise TtsError("tts_quantize_w4_weight", -1)
-    q = torch.empty((N, K // 2), dtype=torch.uint8, device=w_dev.device)
-    s = torch.empty((N, K // 128), dtype=torch.bfloat16, device=w_dev.device)
+    empty, device = _torch().empty, w_dev.device
+    q, s = _fresh(stream, dev, lambda: (empty((N, K // 2), dtype=u8, device=device),
+                                        empty((N, K // 128), dtype=bf16[0], device=device)))
     _call("tts_quantize_w4_weight", w_dev.data_ptr(), N, K, q.data_ptr(), s.data_ptr(), stream)
     return q, s
 
@@ -356,7 +370,8 @@ def attention_decode_kv4(qkv, q_norm, k_norm, k4, v4, k_par, v_par, out, n_q: in
 def code_logprobs(logits, codes, cb_vocab: int, top: int = 0, temperature: float = 1.0, stream=None):
     """tts_code_logprobs: logits fp32 [rows][ld] (rows may be strided) and codes
     int32 [rows][n_cb]; returns (logprob [rows][n_cb], entropy [rows][n_cb],
-    top_codes [rows][n_cb][top], top_logprob [rows][n_cb][top])."""
+    top_codes [rows][n_cb][top], top_logprob [rows][n_cb][top]), made for `stream`
+    (None: the default stream, whatever torch's current one is)."""
     f32, i32, _, _, several = _types or _get_types()
     rows, n_cb = codes.shape
     dev = codes.get_device()
@@ -366,9 +381,10 @@ def code_logprobs(logits, codes, cb_vocab: int, top: int = 0, temperature: float
             or _elsewhere(dev, several)):
         raise TtsError("tts_code_logprobs", -1)
     ld = logits.stride(0) if rows > 1 else logits.shape[1]
-    lp, ent = logits.new_empty((rows, n_cb)), logits.new_empty((rows, n_cb))
-    n = max(top, 0)
-    at, at_lp = codes.new_empty((rows, n_cb, n)), logits.new_empty((rows, n_cb, n))
+    empty, device, n = _torch().empty, codes.device, max(top, 0)
+    lp, ent, at, at_lp = _fresh(stream, dev, lambda: (
+        empty((rows, n_cb), dtype=f32, device=device), empty((rows, n_cb), dtype=f32, device=device),
+        empty((rows, n_cb, n), dtype=i32, device=device), empty((rows, n_cb, n), dtype=f32, device=device)))
     _call("tts_code_logprobs", logits.data_ptr(), ld, codes.data_ptr(), rows, n_cb, cb_vocab, temperature, top,
           lp.data_ptr(), ent.data_ptr(), at.data_ptr() if n else None, at_lp.data_ptr() if n else None, stream)
     return lp, ent, at, at_lp

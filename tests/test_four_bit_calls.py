@@ -76,6 +76,7 @@ def binding(lib, monkeypatch):
     monkeypatch.setattr(m, "_types", None, raising=False)
     monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 0, raising=False)
     return m, seen
 
 

@@ -50,3 +50,50 @@ def test_tensors_of_another_type_size_or_layout_are_refused(ads):
     assert (y == 7.0).all()
     ads.gemv_w4(x, w4, s, y)
     assert ads.code_logprobs(z, codes, 10, top=2)[2].dtype == torch.int32
+
+
+def stream_of(t):
+    """The stream whose memory pool tensor t is of."""
+    import torch
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not the allocator's")
+
+
+def test_results_belong_to_the_stream_they_are_written_on(ads):
+    """The allocator hands memory on in the order of one stream: results made on
+    torch's current stream and written on another could be in use there still."""
+    import torch
+    z, codes = torch.randn((4, 8 * 1026), device="cuda"), torch.zeros((4, 8), dtype=torch.int32, device="cuda")
+    w = torch.randn((64, 512), device="cuda").bfloat16()
+    want, packed = ads.code_logprobs(z, codes, 1026, top=5), ads.quantize_w4_weight(w)
+    torch.cuda.synchronize()
+    current, launch = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(current):
+        for stream in (None, launch.cuda_stream, current.cuda_stream):
+            got = ads.code_logprobs(z, codes, 1026, top=5, stream=stream)
+            q = ads.quantize_w4_weight(w, stream=stream)
+            assert [stream_of(t) for t in (*got, *q)] == [stream or 0] * 6
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip((*got, *q), (*want, *packed)))
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+def test_results_written_beside_a_busy_current_stream(ads):
+    """Memory that the current stream has freed, with its last writes to come, is not
+    handed to results written on another stream."""
+    import torch
+    z, codes = torch.randn((256, 8 * 1026), device="cuda"), torch.zeros((256, 8), dtype=torch.int32, device="cuda")
+    want = ads.code_logprobs(z, codes, 1026, top=5)
+    torch.cuda.synchronize()
+    current, launch = torch.cuda.Stream(), torch.cuda.Stream()
+    with torch.cuda.stream(current):
+        mine = [torch.empty_like(t) for t in want]
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        for t in mine:
+            t.fill_(3)
+        del mine, t
+        got = ads.code_logprobs(z, codes, 1026, top=5, stream=launch.cuda_stream)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
