@@ -49,6 +49,28 @@ inline cudaError_t clusters_at_once(Kernel kern, int threads, size_t smem, int c
     return cudaOccupancyMaxActiveClusters(n, kern, &cfg);
 }
 
+// Memory of a call's arguments (p may be null), and whether anything that the call
+// writes lies over something else of it: other blocks still read what the first ones
+// to finish would write.
+struct Span {
+    const void* p;
+    size_t n;
+};
+inline bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + b.n && y < x + a.n;
+}
+template <size_t W, size_t R>
+inline bool overwritten(const Span (&written)[W], const Span (&read)[R]) {
+    for (size_t i = 0; i < W; ++i) {
+        for (const Span& r : read)
+            if (overlap(written[i], r)) return true;
+        for (size_t j = 0; j < i; ++j)
+            if (overlap(written[i], written[j])) return true;
+    }
+    return false;
+}
+
 // 4-bit codes as operands of fp16 products.  Each 16-bit half of w holds two bytes of
 // two codes: nibble_bytes takes byte 0 of both halves (odd = 0) or byte 1 to the
 // low byte of a half under 0x64, which reads as the fp16 value 1024 + byte.

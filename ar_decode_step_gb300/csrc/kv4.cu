@@ -1092,10 +1092,6 @@ cudaError_t launch_attn_kv4(Kv4Params p, int dev, int sms, cudaStream_t s) {
     return launch_ordered(attn_kv4_kernel<G>, dim3(heads, p.S), dim3(kAttnWarps * 32), kAttnSmem, s, p.cluster ? p.S : 1, 1, p);
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 int report_kv4(cudaError_t e, const char* what) {
@@ -1117,8 +1113,9 @@ bool heads_ok(int n_q, int n_kv) {
     return G == 1 || G == 2 || G == 4 || G == 8;
 }
 
-int rows_ok(const void* k, const void* v, const void* k4, const void* v4, const void* kp, const void* vp, int n_kv,
-            int p0, int p1, int stride, int max_pos) {
+// in: the 4-bit cache is written, else the bf16 ones.
+int rows_ok(bool in, const void* k, const void* v, const void* k4, const void* v4, const void* kp, const void* vp,
+            int n_kv, int p0, int p1, int stride, int max_pos) {
     if (!k || !v || !k4 || !v4 || !kp || !vp || n_kv < 1 || n_kv > kKv4MaxKvHeads) return TTS_ERR_ARG;
     if (max_pos < 1 || max_pos > kKv4MaxPos || p0 < 0 || p1 < p0) return TTS_ERR_ARG;
     if (misaligned(k, 16) || misaligned(v, 16) || misaligned(k4, 16) || misaligned(v4, 16) || misaligned(kp, 16) ||
@@ -1127,10 +1124,9 @@ int rows_ok(const void* k, const void* v, const void* k4, const void* v4, const 
     if (p1 > max_pos) return TTS_ERR_FULL;
     if (p1 > stride) return TTS_ERR_ARG;
     const size_t rows = (size_t)n_kv * max_pos, bytes = (size_t)n_kv * stride * kHeadDim * 2;
-    for (const void* side : {k, v})
-        if (overlap(side, bytes, k4, rows * kRowBytes) || overlap(side, bytes, v4, rows * kRowBytes) ||
-            overlap(side, bytes, kp, rows * 8) || overlap(side, bytes, vp, rows * 8))
-            return TTS_ERR_ARG;
+    const Span wide[] = {{k, bytes}, {v, bytes}};
+    const Span packed[] = {{k4, rows * kRowBytes}, {v4, rows * kRowBytes}, {kp, rows * 8}, {vp, rows * 8}};
+    if (in ? overwritten(packed, wide) : overwritten(wide, packed)) return TTS_ERR_ARG;
     return TTS_OK;
 }
 
@@ -1140,7 +1136,7 @@ int rows_ok(const void* k, const void* v, const void* k4, const void* v4, const 
 extern "C" int tts_quantize_kv4(const void* k, const void* v, int n_kv, int p0, int p1, int src_stride, void* k4,
                                 void* v4, void* k_par, void* v_par, int max_pos, void* stream) {
     using namespace tts;
-    const int rc = rows_ok(k, v, k4, v4, k_par, v_par, n_kv, p0, p1, src_stride, max_pos);
+    const int rc = rows_ok(true, k, v, k4, v4, k_par, v_par, n_kv, p0, p1, src_stride, max_pos);
     if (rc != TTS_OK || p0 == p1) return rc;
     const RowParams p{static_cast<const uint8_t*>(k4),      static_cast<const uint8_t*>(v4),
                       static_cast<const uint32_t*>(k_par),  static_cast<const uint32_t*>(v_par),
@@ -1154,7 +1150,7 @@ extern "C" int tts_quantize_kv4(const void* k, const void* v, int n_kv, int p0, 
 extern "C" int tts_dequantize_kv4(const void* k4, const void* v4, const void* k_par, const void* v_par, int n_kv,
                                   int p0, int p1, int max_pos, void* k, void* v, int dst_stride, void* stream) {
     using namespace tts;
-    const int rc = rows_ok(k, v, k4, v4, k_par, v_par, n_kv, p0, p1, dst_stride, max_pos);
+    const int rc = rows_ok(false, k, v, k4, v4, k_par, v_par, n_kv, p0, p1, dst_stride, max_pos);
     if (rc != TTS_OK || p0 == p1) return rc;
     const RowParams p{static_cast<const uint8_t*>(k4),      static_cast<const uint8_t*>(v4),
                       static_cast<const uint32_t*>(k_par),  static_cast<const uint32_t*>(v_par),
@@ -1185,22 +1181,17 @@ extern "C" int tts_attention_decode_kv4(const float* qkv, const void* q_norm, co
         misaligned(kv_row, 16) || misaligned(workspace, 16))
         return TTS_ERR_ARG;
     if (workspace_bytes < workspace_bytes_for(n_q, n_kv)) return TTS_ERR_ARG;
-    // what one block writes while others still read
     {
         const size_t head = sizeof(float) * kHeadDim, rows = (size_t)n_kv * max_pos;
-        const struct {
-            const void* p;
-            size_t n;
-        } made[] = {{out, n_q * head}, {kv_row, kv_row ? 2 * n_kv * head : 0}, {k4, rows * kRowBytes}, {v4, rows * kRowBytes},
-                    {k_par, rows * 8}, {v_par, rows * 8}, {workspace, workspace_bytes_for(n_q, n_kv)}},
-          read[] = {{qkv, (n_q + 2 * n_kv) * head}, {q_norm, 2 * kHeadDim}, {k_norm, 2 * kHeadDim}};
-        for (size_t i = 0; i < sizeof(made) / sizeof(made[0]); ++i) {
-            if (!made[i].p) continue;
-            for (const auto& r : read)
-                if (overlap(made[i].p, made[i].n, r.p, r.n)) return TTS_ERR_ARG;
-            for (size_t j = 0; j < i; ++j)
-                if (made[j].p && overlap(made[i].p, made[i].n, made[j].p, made[j].n)) return TTS_ERR_ARG;
-        }
+        if (overwritten({{out, n_q * head},
+                         {kv_row, 2 * n_kv * head},
+                         {k4, rows * kRowBytes},
+                         {v4, rows * kRowBytes},
+                         {k_par, rows * 8},
+                         {v_par, rows * 8},
+                         {workspace, workspace_bytes_for(n_q, n_kv)}},
+                        {{qkv, (n_q + 2 * n_kv) * head}, {q_norm, 2 * kHeadDim}, {k_norm, 2 * kHeadDim}}))
+            return TTS_ERR_ARG;
     }
     if (pos >= max_pos) return TTS_ERR_FULL;
     Kv4Params p{};

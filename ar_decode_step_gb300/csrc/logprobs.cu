@@ -491,6 +491,11 @@ extern "C" int tts_code_logprobs(const float* logits, long long ld, const int32_
                           reinterpret_cast<uintptr_t>(logprob) | reinterpret_cast<uintptr_t>(entropy) |
                           reinterpret_cast<uintptr_t>(top_codes) | reinterpret_cast<uintptr_t>(top_logprob);
     if (all & 3) return TTS_ERR_ARG;
+    if (rows > 1 && ld > (1LL << 48) / rows) return TTS_ERR_ARG;  // no memory is that large
+    const size_t n = (size_t)rows * n_cb, row = (size_t)n_cb * cb_vocab;
+    if (overwritten({{logprob, 4 * n}, {entropy, 4 * n}, {top_codes, 4 * n * top}, {top_logprob, 4 * n * top}},
+                    {{logits, 4 * ((size_t)(rows - 1) * ld + row)}, {codes, 4 * n}}))
+        return TTS_ERR_ARG;
     LogprobParams p{logits, ld, codes, rows, n_cb, cb_vocab, 1.f / temperature, top, logprob, entropy, top_codes,
                     top_logprob};
     const cudaError_t e = launch_logprobs(p, static_cast<cudaStream_t>(stream));

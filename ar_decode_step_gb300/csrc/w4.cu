@@ -557,10 +557,6 @@ cudaError_t launch_gemv_w4(const W4Params& p, int dev, int sms, cudaStream_t s) 
     return two ? launch_gemv_w4_as<8, 2>(p, dev, sms, s) : launch_gemv_w4_as<8, 1>(p, dev, sms, s);
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
 int report_w4(cudaError_t e, const char* what) {
@@ -576,6 +572,7 @@ extern "C" int tts_quantize_w4_weight(const void* W, int N, int K, void* W4, voi
     if (!W || !W4 || !s || N < 1 || K < 1 || K % kW4Group) return TTS_ERR_ARG;
     if (misaligned(W, 16) || misaligned(W4, 16) || misaligned(s, 4)) return TTS_ERR_ARG;
     const size_t groups = (size_t)N * (K / kW4Group);
+    if (overwritten({{W4, groups * (kW4Group / 2)}, {s, groups * 2}}, {{W, groups * kW4Group * 2}})) return TTS_ERR_ARG;
     const size_t blocks = (groups + 7) / 8;
     if (blocks > 0x7fffffffu) return TTS_ERR_ARG;
     quantize_w4_kernel<<<(unsigned)blocks, 256, 0, static_cast<cudaStream_t>(stream)>>>(
@@ -595,10 +592,11 @@ extern "C" int tts_gemv_w4(const float* x, const void* W4, const void* s, const 
         misaligned(gamma, 16))
         return TTS_ERR_ARG;
     const size_t yb = sizeof(float) * (size_t)M * N, rows = (size_t)N * (epi == 2 ? 2 : 1);
-    // other blocks still read the inputs while the first ones write y
-    if (overlap(y, yb, x, sizeof(float) * (size_t)M * K) || overlap(y, yb, W4, rows * (K / 2)) ||
-        overlap(y, yb, s, rows * (K / kW4Group) * 2) || (gamma && overlap(y, yb, gamma, 2 * (size_t)K)) ||
-        (resid && resid != y && overlap(y, yb, resid, yb)))
+    if (overwritten({{y, yb}}, {{x, sizeof(float) * (size_t)M * K},
+                                {W4, rows * (K / 2)},
+                                {s, rows * (K / kW4Group) * 2},
+                                {gamma, 2 * (size_t)K},
+                                {resid == y ? nullptr : resid, yb}}))
         return TTS_ERR_ARG;
     W4Params p{x, static_cast<const uint8_t*>(W4), static_cast<const __nv_bfloat16*>(s), resid,
                static_cast<const __nv_bfloat16*>(gamma), y, M, N, K, epi, eps};

@@ -388,9 +388,9 @@ int tts_quantize_fp8_weight(const void* W, int N, int K, void* W8, float* s, voi
  * tts_quantize_w4_weight makes them from W, DEVICE bf16 [N][K]: per group
  * s = bf16(max |w| / 7), u = 8 + clamp(rint(w / s), -8, 7) (IEEE fp32
  * divisions, rounding to nearest even; u = 8 where s is 0).  W finite.
- * K % 128 == 0; W and W4 16-byte, s 4-byte aligned.  Enqueued on `stream` (NULL: the
- * default stream); does not synchronise.  TTS_ERR_ARG for bad sizes, NULL or
- * misaligned pointers. */
+ * K % 128 == 0; W and W4 16-byte, s 4-byte aligned; W4 and s overlap neither W
+ * nor one another.  Enqueued on `stream` (NULL: the default stream); does not
+ * synchronise.  TTS_ERR_ARG otherwise. */
 int tts_quantize_w4_weight(const void* W, int N, int K, void* W4, void* s, void* stream);
 
 /* Stand-alone op: the matrix-vector products of a decode step over 4-bit
@@ -428,8 +428,8 @@ int tts_gemv_w4(const float* x, const void* W4, const void* s, const float* resi
  * n_kv up to 1024.
  * Enqueued on `stream` (NULL: the default stream); neither synchronises.
  * TTS_ERR_FULL if p1 > max_pos; TTS_ERR_ARG if p1 exceeds the bf16 cache's
- * stride, for bad sizes, NULL or misaligned pointers, or where a bf16 cache
- * overlaps the 4-bit one. */
+ * stride, for bad sizes, NULL or misaligned pointers, or where an array that is
+ * written overlaps another argument. */
 int tts_quantize_kv4(const void* k, const void* v, int n_kv, int p0, int p1, int src_stride, void* k4, void* v4,
                      void* k_par, void* v_par, int max_pos, void* stream);
 int tts_dequantize_kv4(const void* k4, const void* v4, const void* k_par, const void* v_par, int n_kv, int p0, int p1,
@@ -478,7 +478,9 @@ int tts_attention_decode_kv4(const float* qkv, const void* q_norm, const void* k
  * entropy are NaN; NaN entries rank last.  DEVICE outputs, fp32 and int32.
  * 0 <= rows (0: nothing is done, pointers may be NULL), 1 <= n_cb <= 8,
  * 2 <= cb_vocab <= 2^20, 0 <= top <= min(32, cb_vocab), temperature positive
- * and finite.  Pointers 4-byte aligned.
+ * and finite.  Pointers 4-byte aligned; outputs overlap neither the logits (from
+ * the first row's first to the last row's last, gaps between rows included), the
+ * codes nor one another.
  * Enqueued on `stream` (NULL: the default stream); does not synchronise; may
  * be captured.  TTS_ERR_ARG otherwise. */
 int tts_code_logprobs(const float* logits, long long ld, const int32_t* codes, int rows, int n_cb, int cb_vocab,

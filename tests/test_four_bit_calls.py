@@ -116,3 +116,38 @@ def test_binding_checks_every_tensor(binding, name):
     with pytest.raises(m.TtsError):  # all on one device, but not the current one
         call(**{n: On(good[n], 1) for n in tensors})
     assert len(seen) == 2
+
+
+# ---- what is written over another argument ----------------------------------------------
+
+def test_quantize_w4_refuses_results_over_the_weights(lib):
+    """A warp writes its group's codes while others still read W."""
+    good = dict(W=A[0], N=16, K=256, W4=A[1], s=A[2], stream=None)
+    for bad in (dict(W4=A[0]), dict(W4=A[0] + 16 * 512 - 16), dict(s=A[0] + 4), dict(s=A[1] + 16 * 128 - 4),
+                dict(W4=A[2] + 48)):
+        assert lib.tts_quantize_w4_weight(*dict(good, **bad).values()) == ARG, bad
+
+
+def test_kv4_rows_refuse_results_over_one_another(lib):
+    """k and v, codes and parameters are written at once."""
+    n = 2 * 16
+    good = dict(k=A[0], v=A[1], n_kv=2, p0=0, p1=8, stride=16, k4=A[2], v4=A[3], k_par=A[4], v_par=A[5], max_pos=16,
+                stream=None)
+    for bad in (dict(v4=A[2]), dict(v4=A[2] + n * 64 - 16), dict(v_par=A[4]), dict(k_par=A[2] + 16),
+                dict(v_par=A[3] + n * 64 - 16), dict(k4=A[5] + n * 8 - 16)):
+        assert lib.tts_quantize_kv4(*dict(good, **bad).values()) == ARG, bad
+    order = ("k4", "v4", "k_par", "v_par", "n_kv", "p0", "p1", "max_pos", "k", "v", "stride", "stream")
+    for bad in (dict(v=A[0]), dict(v=A[0] + n * 256 - 16)):
+        args = dict(good, **bad)
+        assert lib.tts_dequantize_kv4(*(args[a] for a in order)) == ARG, bad
+
+
+def test_code_logprobs_refuses_results_over_the_logits(lib):
+    """A row's results are written while others are read."""
+    row, rows, n = 4 * 8208, 4, 4 * 8
+    for bad in (dict(lp=A[0]), dict(ent=A[0] + rows * row - 4), dict(at=A[0] + row), dict(at_lp=A[0] + 64),
+                dict(lp=A[1]), dict(at=A[1] + 4 * n - 4), dict(ent=A[2]), dict(ent=A[4] + 4 * n * 5 - 4),
+                dict(at_lp=A[3] + 4), dict(at=A[5])):
+        assert lib.tts_code_logprobs(*dict(SCORE, **bad).values()) == ARG, bad
+    # rows further apart than any memory is large
+    assert lib.tts_code_logprobs(*dict(SCORE, ld=1 << 60).values()) == ARG
