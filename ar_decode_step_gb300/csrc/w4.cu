@@ -301,7 +301,8 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
             uint32_t hi[2], lo[2];  // (pair 0, pair 1), (pair 2, pair 3)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float v0 = (a[m][2 * j] - 0.0625f * a[m][2 * j + 1]) * f, v1 = 0.0625f * a[m][2 * j + 1] * f;
+                // (scaled first: a - a' / 16 of the largest numbers would overflow)
+                const float v1 = a[m][2 * j + 1] * (0.0625f * f), v0 = fmaf(a[m][2 * j], f, -v1);
                 const __half2 h = __floats2half2_rn(v0, v1);
                 const float2 hf = __half22float2(h);
                 const __half2 l = __floats2half2_rn(v0 - hf.x, v1 - hf.y);
@@ -399,7 +400,9 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
                             x = d[k][0][2 * h + v] + d[k][1][2 * h + v];
                         else
                             x = (d[k][0][2 * h] + d[k][1][2 * h]) + (d[k][0][2 * h + 1] + d[k][1][2 * h + 1]);
-                        y[h][v] = (h ? sb[k] : sa[k]) * (ap[v] * x);
+                        // the scales first: exact to 2^-149, while the sum of a (u - 8) of
+                        // activations above 2^117 may be beyond fp32
+                        y[h][v] = (h ? sb[k] : sa[k]) * ap[v] * x;
                     }
                 if (MV == 8 || t < MV) {
 #pragma unroll

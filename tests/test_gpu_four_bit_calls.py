@@ -97,3 +97,34 @@ def test_results_written_beside_a_busy_current_stream(ads):
         got = ads.code_logprobs(z, codes, 1026, top=5, stream=launch.cuda_stream)
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def weights(N, K, seed, std=0.02):
+    return ref.quant_w4(synth.normal_bf16(0, seed, (N, K), std=std))
+
+
+def near(got, want, tol):
+    err = np.abs(got.astype(np.float64) - want)
+    assert np.isfinite(got).all() and (err <= tol).all(), (err / tol).max()
+
+
+def dev(a):
+    import torch
+    a = np.ascontiguousarray(a)
+    return torch.from_numpy(a.view(np.int16) if a.dtype == np.uint16 else a).cuda()
+
+
+@pytest.mark.parametrize("M,N,K,epi", [(1, 40, 256, 0), (2, 40, 512, 1), (4, 33, 1280, 0), (7, 64, 384, 0), (8, 2560, 9728, 0)])
+def test_gemv_w4_activations_up_to_the_largest_number(ads, M, N, K, epi):
+    """Activations next to fp32's end under weights that bring the products back:
+    neither a pair's combination nor a group's sum before its scale overflows."""
+    import torch
+    b, s = weights(N, K, 41, std=1e-6)
+    rng = np.random.default_rng(K)
+    x = (rng.uniform(2.5e38, 3.4e38, (M, K)) * rng.choice([-1.0, 1.0], (M, K))).astype(np.float32)
+    x[-1, 128:] *= np.float32(1e-30)
+    resid = (rng.standard_normal((M, N)) * 1e32).astype(np.float32) if epi else None
+    want, tol = ref.gemv_w4(x, b, s, epi, resid)
+    y = torch.empty((M, N), device="cuda")
+    ads.gemv_w4(dev(x), dev(b), dev(s), y, epi, None if resid is None else dev(resid))
+    near(y.cpu().numpy(), want, tol)
