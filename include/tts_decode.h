@@ -401,9 +401,12 @@ int tts_quantize_w4_weight(const void* W, int N, int K, void* W4, void* s, void*
  *   epi 0: y = a . W^T; epi 1: y = resid + a . W^T; epi 2: SwiGLU,
  *   y = silu(a . gate^T) * (a . up^T).  y: DEVICE fp32 [M][N]; resid: DEVICE
  *   fp32 [M][N] for epi 1 (may be y itself), NULL otherwise.
- * Activations stay fp32 (as two fp16 parts, 22 bits), sums are fp32, and every
- * result is deterministic.  1 <= M <= 8, K % 128 == 0, 128 <= K <= 12288, any
- * N from 1 to 2^24.  x, W4 and gamma 16-byte, s 4-byte aligned; y overlaps no input
+ * An activation takes part with 22 bits, as two fp16 numbers under its 128
+ * group's power of two (and to no less than 2^-39 of the group's largest); sums
+ * are fp32, and results do not depend on the run.  A vector whose a holds a NaN
+ * or an infinity, x * gamma beyond fp32 included, has NaN in all its results;
+ * mean(x^2) is fp32 as well, |x| below 2^57 with gamma.
+ * 1 <= M <= 8, K % 128 == 0, 128 <= K <= 12288, any N from 1 to 2^24.  x, W4 and gamma 16-byte, s 4-byte aligned; y overlaps no input
  * (but resid == y).  Enqueued on `stream` (NULL: the default stream); does
  * not synchronise; may be captured.  TTS_ERR_ARG otherwise. */
 int tts_gemv_w4(const float* x, const void* W4, const void* s, const float* resid, const void* gamma, float* y, int M,

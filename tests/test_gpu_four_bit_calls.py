@@ -128,3 +128,24 @@ def test_gemv_w4_activations_up_to_the_largest_number(ads, M, N, K, epi):
     y = torch.empty((M, N), device="cuda")
     ads.gemv_w4(dev(x), dev(b), dev(s), y, epi, None if resid is None else dev(resid))
     near(y.cpu().numpy(), want, tol)
+
+
+@pytest.mark.parametrize("M", [1, 2, 4, 8])
+@pytest.mark.parametrize("N,K,epi,norm", [(40, 256, 0, False), (40, 256, 2, True), (2560, 9728, 1, False), (17, 12288, 0, True)])
+def test_gemv_w4_a_vector_with_a_non_finite_activation_is_nan(ads, M, N, K, epi, norm):
+    """All of its results, whatever the weights there, and none of the others'."""
+    import torch
+    b, s = weights(2 * N if epi == 2 else N, K, 43)
+    gamma = synth.normal_bf16(3, 44, (K,), std=0.02, mean=1.0) if norm else None
+    resid = synth.normal_f32(5, 45, (M, N)) if epi == 1 else None
+    clean = synth.normal_f32(5, 46, (M, K))
+    want, tol = ref.gemv_w4(clean, b, s, epi, resid, gamma)
+    for at, (bad, k) in enumerate([(np.nan, 0), (np.inf, K - 1), (-np.inf, K // 2), (np.nan, 129 % K)]):
+        x, m = clean.copy(), at % M
+        x[m, k] = bad
+        y = torch.zeros((M, N), device="cuda")
+        ads.gemv_w4(dev(x), dev(b), dev(s), y, epi, None if resid is None else dev(resid), None if gamma is None else dev(gamma))
+        y = y.cpu().numpy()
+        assert np.isnan(y[m]).all(), (bad, k)
+        others = np.arange(M) != m
+        near(y[others], want[others], tol[others]) if others.any() else None
