@@ -71,6 +71,24 @@ inline bool overwritten(const Span (&written)[W], const Span (&read)[R]) {
     return false;
 }
 
+// Whether the first phase of a barrier is over, its copies there.  A wait's limit is
+// wall time, which also passes while the GPU is another process's: one that ran out
+// is made once more before the copies count as lost (on their way they take
+// microseconds).
+__device__ __forceinline__ bool mbar_arrived(uint64_t* bar) {
+    if (mbar_try_wait(bar, 0)) return true;
+    uint64_t t0 = globaltimer_ns();
+    bool again = true;
+    while (!mbar_try_wait(bar, 0)) {
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            if (!again) return false;
+            again = false;
+            t0 = globaltimer_ns();
+        }
+    }
+    return true;
+}
+
 // 4-bit codes as operands of fp16 products.  Each 16-bit half of w holds two bytes of
 // two codes: nibble_bytes takes byte 0 of both halves (odd = 0) or byte 1 to the
 // low byte of a half under 0x64, which reads as the fp16 value 1024 + byte.

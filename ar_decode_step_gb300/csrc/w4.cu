@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
             if (g == g0) {
 #pragma unroll
                 for (int k = 0; k < n; ++k)
-                    if (!mbar_wait(&bars[q + k], 0)) late = 1;
+                    if (!mbar_arrived(&bars[q + k])) late = 1;
             }
             uint4 wa[n], wb[n];
             float sa[n], sb[n], d[n][2][4];
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
     if (!kInAct && g0 == g1)  // no group: nothing of this warp's, but its copies
         for (int i = lane; i < outs * PARTS; i += 32) sums[i] = 0.f;
     for (int q = 0; q < nt * PARTS; ++q)
-        if (g0 == g1 && !mbar_wait(&bars[q], 0)) late = 1;
+        if (g0 == g1 && !mbar_arrived(&bars[q])) late = 1;
     __syncthreads();
     if (late)  // a copy may still be on its way: once more, again with a limit
         for (int q = 0; q < nt * PARTS; ++q) mbar_wait(&bars[q], 0);

@@ -406,8 +406,10 @@ int tts_quantize_w4_weight(const void* W, int N, int K, void* W4, void* s, void*
  * are fp32, and results do not depend on the run.  A vector whose a holds a NaN
  * or an infinity, x * gamma beyond fp32 included, has NaN in all its results;
  * mean(x^2) is fp32 as well, |x| below 2^57 with gamma.
- * 1 <= M <= 8, K % 128 == 0, 128 <= K <= 12288, any N from 1 to 2^24.  x, W4 and gamma 16-byte, s 4-byte aligned; y overlaps no input
- * (but resid == y).  Enqueued on `stream` (NULL: the default stream); does
+ * Waits inside the kernel are bounded: where weights have not arrived within two
+ * limits of 1 s, outputs that need them are NaN.
+ * 1 <= M <= 8, K % 128 == 0, 128 <= K <= 12288, any N from 1 to 2^24.  x, W4 and
+ * gamma 16-byte, s 4-byte aligned; y overlaps no input (but resid == y).  Enqueued on `stream` (NULL: the default stream); does
  * not synchronise; may be captured.  TTS_ERR_ARG otherwise. */
 int tts_gemv_w4(const float* x, const void* W4, const void* s, const float* resid, const void* gamma, float* y, int M,
                 int N, int K, int epi, float eps, void* stream);

@@ -149,3 +149,20 @@ def test_gemv_w4_a_vector_with_a_non_finite_activation_is_nan(ads, M, N, K, epi,
         assert np.isnan(y[m]).all(), (bad, k)
         others = np.arange(M) != m
         near(y[others], want[others], tol[others]) if others.any() else None
+
+
+def test_a_late_copy_is_waited_for_a_second_time(tmp_path):
+    """A kernel that was off the GPU for longer than a wait's limit finds its
+    copies at the second wait (here an arrival 1.3 s late; limits are 1 s)."""
+    import os
+    import shutil
+    import subprocess
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    exe = str(tmp_path / "check")
+    subprocess.run([shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc", "-std=c++17", "-O2", "-gencode",
+                    "arch=compute_103a,code=sm_103a", "--expt-relaxed-constexpr", "-I", os.path.join(root, "include"), "-I",
+                    os.path.join(root, "ar_decode_step_gb300", "csrc"),
+                    os.path.join(root, "tests", "host", "mbar_arrived_check.cu"), "-o", exe],
+                   check=True, capture_output=True, text=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr
