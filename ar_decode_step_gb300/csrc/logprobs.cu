@@ -442,6 +442,31 @@ __global__ void __launch_bounds__(kLongWarps * 32, 2) logprobs_long_kernel(const
     finish(p, item, z, r, list_v, list_i);
 }
 
+// How a long row is shared: warps a block, blocks a row.
+struct LongPlan {
+    int warps, blocks;
+};
+LongPlan plan_long(int items, int V, int sms) {
+    // Warps a row, each with its runs in turn: the least rounds of blocks (32 warps
+    // an SM) times turns, and of equals the fewest, four at least, as there are fewer
+    // lists to merge and few entries of a later run are above a warp's list.  (20
+    // alternatives: 512 x 32000 8 warps 25.3 us, 11 warps 30.4, 16 warps 28.6;
+    // 2000 x 8192 4 warps 26.4, 2 warps 27.8, 8 warps 32.9.)
+    const int runs = (V + kRun - 1) / kRun;
+    int W = std::min(kLongWarps, runs);
+    const auto cost = [&](int w) {
+        const long long at_once = (long long)sms * (32 / w);
+        return (items + at_once - 1) / at_once * ((runs + w - 1) / w);
+    };
+    for (int w = W - 1; w >= 4; --w)
+        if (cost(w) <= cost(W)) W = w;
+    // one block a row, or so many that every warp has one run, while the rows do
+    // not fill the SMs by themselves
+    int C = 1;
+    while (C < 8 && C * W < runs && (long long)items * C < sms) C *= 2;
+    return LongPlan{W, C};
+}
+
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t s) {
@@ -453,23 +478,12 @@ cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t s) {
         return launch_ordered(p.V <= 256 ? logprobs_short_kernel<8> : logprobs_short_kernel<kRunNv>, dim3(grid),
                               dim3(kShortWarps * 32), 0, s, 1, 1, p, items);
     }
-    // Warps a row, each with its runs in turn: the least rounds of blocks (32 warps
-    // an SM) times turns, and of equals the fewest, four at least, as there are fewer
-    // lists to merge and few entries of a later run are above a warp's list.  (20
-    // alternatives: 512 x 32000 8 warps 25.3 us, 11 warps 30.4, 16 warps 28.6;
-    // 2000 x 8192 4 warps 26.4, 2 warps 27.8, 8 warps 32.9.)
-    const int runs = (p.V + kRun - 1) / kRun;
-    int W = std::min(kLongWarps, runs);
-    const auto cost = [&](int w) {
-        const long long at_once = 152 * (32 / w);
-        return (items + at_once - 1) / at_once * ((runs + w - 1) / w);
-    };
-    for (int w = W - 1; w >= 4; --w)
-        if (cost(w) <= cost(W)) W = w;
-    // one block a row, or so many that every warp has one run, while the rows do
-    // not fill the SMs by themselves
-    int C = 1;
-    while (C < 8 && C * W < runs && (long long)items * C < 152) C *= 2;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const LongPlan plan = plan_long(items, p.V, sms);
+    const int W = plan.warps, C = plan.blocks;
     const size_t smem = sizeof(Candidates) * (W + (C > 1 ? C : 0));
     return launch_ordered(logprobs_long_kernel, dim3(items, C), dim3(W * 32), smem, s, C, 1, p);
 }
