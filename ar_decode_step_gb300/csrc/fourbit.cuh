@@ -146,7 +146,7 @@ struct LogprobParams {
     long long ld;
     const int* codes;     // [rows][n_cb], or null
     int rows, n_cb, V;
-    float inv_t;          // 1 / temperature
+    float two_over_t;     // 2 / temperature
     int top;
     float* logprob;       // [rows][n_cb], or null
     float* entropy;       // [rows][n_cb], or null

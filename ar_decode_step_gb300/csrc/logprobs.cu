@@ -10,6 +10,7 @@
 // there are few rows, whose results are joined through shared memory in a
 // fixed order, as a softmax over parts is.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstdio>
@@ -22,7 +23,7 @@
 namespace tts {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kRunNv = 33;                // 33 values a lane: 1026-entry codebooks in one run
 constexpr int kRun = 32 * kRunNv;
@@ -40,6 +41,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float max_nan(float x, float y) {  // NaN where one is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
 // fp32 bits (no NaN) as unsigned integers in the order of the values; -0 is 0.
 __device__ __forceinline__ uint32_t ranked(float z) {
     const uint32_t b = __float_as_uint(z + 0.f);
@@ -50,19 +56,22 @@ __device__ __forceinline__ float from_ranked(uint32_t k) {
 }
 constexpr uint32_t kRankedNone = 0x007fffffu;  // of -inf
 
-// What a part of a row comes to, its NaN entries left out: maximum m, l = sum
-// e^((z - m) / T), w = sum (z - m) e^((z - m) / T), and whether there was a NaN.
-// l = 0 where nothing is above -inf (and where m = +inf, which the caller sees).
+// Differences of logits are taken halved, z / 2 - m / 2, which no pair of finite
+// logits overflows, and times c = 2 log2(e) / T they are t = log2(e) (z - m) / T.
+__device__ __forceinline__ float halved(float z, float m) { return fmaf(0.5f, z, -0.5f * m); }
+
+// What a part of a row comes to, its NaN entries left out: maximum m, l = sum 2^t, w =
+// sum t 2^t, and whether there was a NaN.  l = 0 where nothing is above -inf (and where
+// m = +inf, which the caller sees).
 struct Part {
     float m, l, w;
     int nan;
 };
-// c = log2(e) / T.
 __device__ __forceinline__ Part join(const Part& a, const Part& b, float c) {
     const float m = fmaxf(a.m, b.m);
-    const float da = fmaxf(a.m - m, -3.0e38f), db = fmaxf(b.m - m, -3.0e38f);
-    const float fa = a.l > 0.f ? ex2(da * c) : 0.f, fb = b.l > 0.f ? ex2(db * c) : 0.f;
-    return Part{m, fa * a.l + fb * b.l, (fa > 0.f ? fa * (a.w + da * a.l) : 0.f) + (fb > 0.f ? fb * (b.w + db * b.l) : 0.f),
+    const float ta = halved(a.m, m) * c, tb = halved(b.m, m) * c;
+    const float fa = a.l > 0.f ? ex2(ta) : 0.f, fb = b.l > 0.f ? ex2(tb) : 0.f;
+    return Part{m, fa * a.l + fb * b.l, (fa > 0.f ? fa * fmaf(ta, a.l, a.w) : 0.f) + (fb > 0.f ? fb * fmaf(tb, b.l, b.w) : 0.f),
                 a.nan | b.nan};
 }
 // All lanes' parts joined, lane order fixed.
@@ -162,15 +171,16 @@ __device__ __forceinline__ Part warp_run(const float* z, int n, int first, float
     r.m = from_ranked(__reduce_max_sync(kAll, ranked(m)));
     r.l = r.w = 0.f;
     if (r.m != -INFINITY && r.m != INFINITY) {
-        const f32x2 minus = pack2(-r.m, -r.m), cc = pack2(c, c);
+        const f32x2 half = pack2(0.5f, 0.5f), minus = pack2(-0.5f * r.m, -0.5f * r.m), cc = pack2(c, c);
         f32x2 l = pack2(0.f, 0.f), w = l;
 #pragma unroll
         for (int i = 0; i < NV; i += 2) {
-            const f32x2 d = add2(pack2(v[i], v[i + 1]), minus);
-            const float2 a = unpack2(mul2(d, cc)), b = unpack2(d);
-            const f32x2 e = pack2(ex2(a.x), ex2(a.y));
-            l = add2(l, e);                                                    // NaN where an entry is NaN
-            w = fma2(e, pack2(fmaxf(b.x, -3.0e38f), fmaxf(b.y, -3.0e38f)), w);  // an entry of -inf adds 0
+            // 2^-200 is 0: an entry of -inf adds 0 to w as to l.  A NaN makes both NaN
+            const float2 far = unpack2(mul2(fma2(pack2(v[i], v[i + 1]), half, minus), cc));
+            const float2 t = make_float2(max_nan(far.x, -200.f), max_nan(far.y, -200.f));
+            const f32x2 e = pack2(ex2(t.x), ex2(t.y));
+            l = add2(l, e);
+            w = fma2(e, pack2(t.x, t.y), w);
         }
         const float2 ls = unpack2(l), wsum = unpack2(w);
         r.l = warp_sum(ls.x + ls.y);
@@ -353,13 +363,14 @@ __device__ __forceinline__ void finish(const LogprobParams& p, size_t item, cons
     const int lane = threadIdx.x & 31;
     const bool bad = r.nan || r.m == INFINITY, none = !bad && r.m == -INFINITY;
     const float logl = logf(r.l);
-    auto logp = [&](float x) { return bad ? NAN : none ? -INFINITY : (x - r.m) * p.inv_t - logl; };
+    auto logp = [&](float x) { return bad ? NAN : none ? -INFINITY : fmaf(halved(x, r.m), p.two_over_t, -logl); };
     if (lane == 0) {
         if (p.logprob) {
-            const int c = p.codes[item];
-            p.logprob[item] = c < 0 || c >= p.V ? NAN : logp(z[c]);
+            const int code = p.codes[item];
+            p.logprob[item] = code < 0 || code >= p.V ? NAN : logp(z[code]);
         }
-        if (p.entropy) p.entropy[item] = bad ? NAN : none ? 0.f : logl - r.w / r.l * p.inv_t;
+        // (the quotient to 2 ulp: as exact as the sums, and 0.2 us less for 4096 frames)
+        if (p.entropy) p.entropy[item] = bad ? NAN : none ? 0.f : logl - __fdividef(r.w, r.l) * kLn2;
     }
     if (p.top == 0) return;
     int got = __popc(__ballot_sync(kAll, lane < p.top && list_v != -INFINITY));
@@ -393,7 +404,7 @@ __global__ void __launch_bounds__(kShortWarps * 32) logprobs_short_kernel(const 
     const float* z = row_of(p, item);
     float list_v = -INFINITY;
     int list_i = 0;
-    const Part r = warp_run<NV, false>(z, p.V, 0, kLog2e * p.inv_t, p.top, cand[threadIdx.x >> 5], list_v, list_i);
+    const Part r = warp_run<NV, false>(z, p.V, 0, kLog2e * p.two_over_t, p.top, cand[threadIdx.x >> 5], list_v, list_i);
     finish(p, item, z, r, list_v, list_i);
 }
 
@@ -412,7 +423,7 @@ __global__ void __launch_bounds__(kLongWarps * 32, 2) logprobs_long_kernel(const
     pdl_wait();
     const size_t item = blockIdx.x;
     const float* z = row_of(p, item);
-    const float c = kLog2e * p.inv_t;
+    const float c = kLog2e * p.two_over_t;
     Part r{-INFINITY, 0.f, 0.f, 0};
     float list_v = -INFINITY;
     int list_i = 0;
@@ -497,7 +508,7 @@ extern "C" int tts_code_logprobs(const float* logits, long long ld, const int32_
     if (rows < 0 || n_cb < 1 || n_cb > kMaxCodebooks || cb_vocab < 2 || cb_vocab > (1 << 20)) return TTS_ERR_ARG;
     if (ld < (long long)n_cb * cb_vocab || top < 0 || top > kMaxTop || top > cb_vocab) return TTS_ERR_ARG;
     if ((long long)rows * n_cb > 0x7fffffffLL - kShortWarps) return TTS_ERR_ARG;
-    if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(kLog2e / temperature)) return TTS_ERR_ARG;
+    if (!(temperature >= FLT_MIN) || !std::isfinite(temperature)) return TTS_ERR_ARG;
     if (rows == 0) return TTS_OK;  // an empty array may have no address
     if (!logits || (logprob != nullptr) != (codes != nullptr)) return TTS_ERR_ARG;
     if ((top > 0) != (top_codes != nullptr) || (top > 0) != (top_logprob != nullptr)) return TTS_ERR_ARG;
@@ -510,7 +521,7 @@ extern "C" int tts_code_logprobs(const float* logits, long long ld, const int32_
     if (overwritten({{logprob, 4 * n}, {entropy, 4 * n}, {top_codes, 4 * n * top}, {top_logprob, 4 * n * top}},
                     {{logits, 4 * ((size_t)(rows - 1) * ld + row)}, {codes, 4 * n}}))
         return TTS_ERR_ARG;
-    LogprobParams p{logits, ld, codes, rows, n_cb, cb_vocab, 1.f / temperature, top, logprob, entropy, top_codes,
+    LogprobParams p{logits, ld, codes, rows, n_cb, cb_vocab, 2.f / temperature, top, logprob, entropy, top_codes,
                     top_logprob};
     const cudaError_t e = launch_logprobs(p, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) return TTS_OK;

@@ -482,8 +482,8 @@ int tts_attention_decode_kv4(const float* qkv, const void* q_norm, const void* k
  * With a NaN or +inf among its logits a codebook's log probabilities and
  * entropy are NaN; NaN entries rank last.  DEVICE outputs, fp32 and int32.
  * 0 <= rows (0: nothing is done, pointers may be NULL), 1 <= n_cb <= 8,
- * 2 <= cb_vocab <= 2^20, 0 <= top <= min(32, cb_vocab), temperature positive
- * and finite.  Pointers 4-byte aligned; outputs overlap neither the logits (from
+ * 2 <= cb_vocab <= 2^20, 0 <= top <= min(32, cb_vocab), temperature finite and
+ * at least 2^-126.  Pointers 4-byte aligned; outputs overlap neither the logits (from
  * the first row's first to the last row's last, gaps between rows included), the
  * codes nor one another.
  * Enqueued on `stream` (NULL: the default stream); does not synchronise; may

@@ -151,3 +151,12 @@ def test_code_logprobs_refuses_results_over_the_logits(lib):
         assert lib.tts_code_logprobs(*dict(SCORE, **bad).values()) == ARG, bad
     # rows further apart than any memory is large
     assert lib.tts_code_logprobs(*dict(SCORE, ld=1 << 60).values()) == ARG
+
+
+def test_code_logprobs_takes_temperatures_that_are_normal_numbers(lib):
+    """2 log2(e) / T has to be finite: from the smallest normal number on."""
+    none = dict(SCORE, z=None, codes=None, rows=0, lp=None, ent=None, at=None, at_lp=None)
+    for T in (2.0 ** -126, 1e-37, 1e38, 3.4e38):
+        assert lib.tts_code_logprobs(*dict(none, T=T).values()) == 0
+    for T in (1.1e-38, 6e-39, 1e-45, -1e-37):
+        assert lib.tts_code_logprobs(*dict(none, T=T).values()) == ARG, T

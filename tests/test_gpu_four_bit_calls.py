@@ -166,3 +166,24 @@ def test_a_late_copy_is_waited_for_a_second_time(tmp_path):
                    check=True, capture_output=True, text=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("V", [40, 1026, 9001, 70000])
+@pytest.mark.parametrize("T,scale", [(1e30, 1e30), (1e37, 3e37), (3e38, 1e38), (1e-37, 1e-37), (2.0 ** -126, 2.0 ** -126)])
+def test_code_logprobs_at_extreme_temperatures(ads, V, T, scale):
+    """Logits and temperatures at both ends of fp32, whose quotients are ordinary:
+    neither a difference of two logits nor the entropy's sum overflows."""
+    import torch
+    T = float(np.float32(T))
+    z = np.clip(synth.normal_f32(7, V, (5, 2, V), std=2.5).astype(np.float64) * scale, -3.4e38, 3.4e38).astype(np.float32)
+    z[1, 0, ::5] = -np.inf
+    z[2, 0, :2] = np.float32(3.4e38) * np.float32([1, -1]) if scale > 1 else z[2, 0, :2]
+    codes = np.random.default_rng(V).integers(0, V, (5, 2)).astype(np.int32)
+    codes[2, 0] = 1
+    lp, ent, at, at_lp, t_lp, t_ent, t_at = ref.code_logprobs(z, codes, 7, T)
+    got = [t.cpu().numpy() for t in ads.code_logprobs(dev(z.reshape(5, -1)), dev(codes), V, top=7, temperature=T)]
+    for g, w, t in ((got[0], lp, t_lp), (got[1], ent, t_ent), (got[3], at_lp, t_at)):
+        fine = np.isfinite(w)
+        assert np.array_equal(g[~fine], w[~fine]) and (np.abs(g[fine] - w[fine]) <= t[fine]).all(), \
+            (np.abs(g[fine] - w[fine]) / t[fine]).max()
+    assert np.array_equal(got[2], at)
