@@ -187,3 +187,106 @@ def test_code_logprobs_at_extreme_temperatures(ads, V, T, scale):
         assert np.array_equal(g[~fine], w[~fine]) and (np.abs(g[fine] - w[fine]) <= t[fine]).all(), \
             (np.abs(g[fine] - w[fine]) / t[fine]).max()
     assert np.array_equal(got[2], at)
+
+
+FIRST = """
+import sys
+sys.path[:0] = [{root!r}, {root!r} + "/tests"]
+import numpy as np, torch
+import ar_decode_step_gb300 as ads
+ads.load()
+g = torch.Generator(device="cuda").manual_seed(1)
+f = lambda *s: torch.randn(s, generator=g, device="cuda")
+u = lambda *s: torch.randint(0, 256, s, generator=g, device="cuda", dtype=torch.uint8)
+b = lambda *s: f(*s).bfloat16()
+n_kv, n = 2, 9001
+cache = [u(n_kv, n, 64), u(n_kv, n, 64), b(n_kv, n, 2, 2).abs(), b(n_kv, n, 2, 2)]
+rows, back = [b(n_kv, 40, 128) for _ in range(2)], [b(n_kv, 40, 128) for _ in range(2)]
+ws = torch.zeros(ads.kv4_workspace_bytes(16, n_kv), dtype=torch.uint8, device="cuda")
+qkv, gains, outs = f(20 * 128), [b(128), b(128)], [f(16 * 128) for _ in range(3)]
+x, w, s, y = f(8, 9728), u(2560, 4864), b(2560, 76).abs(), f(8, 2560)
+w2, s2, y2 = u(2 * 700, 128), b(2 * 700, 2).abs(), f(1, 700)
+z, codes = f(3, 8 * 1026), torch.randint(0, 1026, (3, 8), generator=g, device="cuda", dtype=torch.int32)
+zl, cl = f(2, 70000), torch.randint(0, 70000, (2, 1), generator=g, device="cuda", dtype=torch.int32)
+wb = b(32, 256)
+
+
+def every(stream):
+    k4, v4, kp, vp = cache
+    ads.quantize_kv4(*rows, k4, v4, kp, vp, 0, 40, stream=stream)
+    for o, pos in zip(outs, (20, 1000, 9000)):
+        ads.attention_decode_kv4(qkv, *gains, k4, v4, kp, vp, o, 16, n_kv, pos, ws, stream=stream)
+    ads.dequantize_kv4(k4, v4, kp, vp, *back, 0, 40, stream=stream)
+    ads.gemv_w4(x, w, s, y, stream=stream)
+    ads.gemv_w4(x[:1, :256].contiguous() if stream is None else x1, w2, s2, y2, epi=2, stream=stream)
+    return [*ads.code_logprobs(z, codes, 1026, top=5, stream=stream), *ads.code_logprobs(zl, cl, 70000, top=20, stream=stream),
+            *ads.quantize_w4_weight(wb, stream=stream), *outs, *back, y, y2]
+
+
+x1 = x[:1, :256].contiguous()
+torch.cuda.synchronize()
+side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=side):
+    got = every(side.cuda_stream)
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+want = every(None)
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip(got, want)), [torch.equal(p, q) for p, q in zip(got, want)]
+assert all(torch.isfinite(t.float()).all() for t in want)
+print("same", len(want))
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """What a call prepares once per device (limits, room for clusters, the module
+    itself) may be prepared while a stream is being captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout + r.stderr[-2000:]
+
+
+def test_calls_from_two_threads(ads):
+    """Each with its stream, tensors and workspace: the answers are those of one after the other."""
+    import threading
+    import torch
+    n_q, n_kv, n = 16, 2, 5001
+    made = []
+    for i in range(2):
+        k4 = torch.randint(0, 256, (n_kv, n, 64), device="cuda", dtype=torch.uint8)
+        par = torch.rand((n_kv, n, 2, 2), device="cuda").bfloat16()
+        made.append(dict(k4=k4, v4=k4.flip(1).contiguous(), k_par=par, v_par=par.flip(1).contiguous(),
+                         qkv=torch.randn((n_q + 2 * n_kv) * D, device="cuda"), q_norm=torch.ones(D, device="cuda").bfloat16(),
+                         k_norm=torch.ones(D, device="cuda").bfloat16(), out=torch.zeros(n_q * D, device="cuda"), n_q=n_q,
+                         n_kv=n_kv, pos=n - 1 - 2000 * i,
+                         workspace=torch.zeros(ads.kv4_workspace_bytes(n_q, n_kv), dtype=torch.uint8, device="cuda")))
+    x, w = torch.randn((4, 2560), device="cuda"), torch.randint(0, 256, (256, 1280), device="cuda", dtype=torch.uint8)
+    s = torch.rand((256, 20), device="cuda").bfloat16()
+    want = []
+    for m in made:
+        ads.attention_decode_kv4(**m)
+        y = torch.zeros((4, 256), device="cuda")
+        ads.gemv_w4(x, w, s, y)
+        torch.cuda.synchronize()
+        want.append((m["out"].clone(), y))
+    wrong = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        y = torch.zeros((4, 256), device="cuda")
+        torch.cuda.synchronize()
+        for _ in range(200):
+            ads.attention_decode_kv4(**made[i], stream=stream.cuda_stream)
+            ads.gemv_w4(x, w, s, y, stream=stream.cuda_stream)
+        stream.synchronize()
+        if not (torch.equal(made[i]["out"], want[i][0]) and torch.equal(y, want[i][1])):
+            wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not wrong
