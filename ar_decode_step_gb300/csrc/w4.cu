@@ -115,31 +115,34 @@ __device__ __forceinline__ void mma16816_f16_first(float c[4], uint32_t a0, uint
 // warps][sums of squares: MV x warps][totals of the block: outputs x parts, MV].
 __host__ __device__ constexpr int columns_of(int mv) { return 2 * mv; }
 __host__ __device__ constexpr int act_group_bytes(int mv) { return 4 * columns_of(mv) * 64; }
-// Whether a warp's sums take the place of its first group's activations, which are
-// in registers by then.  It brings gate/up of four vectors at 2560 x 9728 to one
-// block an SM (10.2 us against 14.8); elsewhere room is left or nothing is gained,
-// and a place of their own is 2 to 9 % faster.
-__host__ __device__ constexpr bool sums_in_act(int mv, int parts) { return mv == 4 && parts == 2; }
+// Kernels of four vectors with a gate and an up tile come in two forms: a warp's sums in
+// a place of their own, or (in_act) where its first group's activations were, which
+// are in registers by then.  The second is 5 to 17 % slower at equal plans (gate/up
+// 6144 x 2560 8.2 us against 7.7, 4096 x 2048 5.9 and 5.5, 2560 x 9728 20.7 and 17.4)
+// and saves 21 KB a block for four tiles: it is taken where that saves a round of
+// blocks (9728 x 2560 10.2 against 14.7, 16384 x 2560 19.0 and 22.1).  Elsewhere a
+// round is not to be had.
+__host__ __device__ constexpr bool has_in_act(int mv, int parts) { return mv == 4 && parts == 2; }
 // (20 at eight vectors, in 96 registers, took 8.6 us instead of 8.2 on 8208 x 2560.)
 __host__ __device__ constexpr int max_warps(int mv) { return mv == 8 ? 16 : 20; }
 __host__ __device__ inline int row_pitch(int share) { return share * 64 + (share & 1 ? 0 : 64); }
 struct W4Smem {
     uint32_t act, par, scales, sums, sq, tot, total;
 };
-__host__ __device__ inline W4Smem smem_of(int mv, int parts, int tiles, int share, int warps) {
+__host__ __device__ inline W4Smem smem_of(int mv, int parts, bool in_act, int tiles, int share, int warps) {
     W4Smem o;
     const uint32_t outs = tiles * 16 * mv * parts;
     o.act = tiles * parts * 16 * row_pitch(share);
     o.par = o.act + share * act_group_bytes(mv);
     o.scales = (o.par + share * mv * 4 + 15) & ~15u;
     o.sums = o.scales + tiles * parts * share * 32;
-    o.sq = o.sums + (sums_in_act(mv, parts) ? 0 : outs * warps * 4);
+    o.sq = o.sums + (in_act ? 0 : outs * warps * 4);
     o.tot = o.sq + mv * warps * 4;
     o.total = o.tot + (outs + mv) * 4;
     return o;
 }
 
-template <int MV, int PARTS>  // vectors (1, 2, 4, 8), tiles an output tile takes
+template <int MV, int PARTS, bool IN_ACT>  // vectors (1, 2, 4, 8), tiles an output tile takes, the sums' place
 __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4Params p, const W4Launch c) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kMaxTiles * PARTS];
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
     // this block's tiles: tile0, tile0 + step, ...
     const int nt = c.tiles - ((long long)tile0 + (long long)(c.tiles - 1) * step >= ntiles);
     const int pitch = row_pitch(c.share);
-    const W4Smem o = smem_of(MV, PARTS, c.tiles, c.share, W);
+    const W4Smem o = smem_of(MV, PARTS, IN_ACT, c.tiles, c.share, W);
 
     // ---- activations of the slice's first group, then the copies
     float4 xs[MV];
@@ -329,9 +332,8 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
     __syncthreads();  // the scales come from other warps
 
     // ---- the products: a group's activations in registers, all tiles past them
-    constexpr bool kInAct = sums_in_act(MV, PARTS);
-    static_assert(!kInAct || kMaxTiles / 2 * 16 * MV * PARTS * 4 <= act_group_bytes(MV), "a warp's sums fit a group");
-    float* sums = kInAct ? reinterpret_cast<float*>(smem + o.act + g0 * act_group_bytes(MV))
+    static_assert(!IN_ACT || kMaxTiles / 2 * 16 * MV * PARTS * 4 <= act_group_bytes(MV), "a warp's sums fit a group");
+    float* sums = IN_ACT ? reinterpret_cast<float*>(smem + o.act + g0 * act_group_bytes(MV))
                          : reinterpret_cast<float*>(smem + o.sums) + (size_t)warp * outs * PARTS;  // [tile x parts][row][vector]
     const bool column = MV == 8 || r < 2 * MV;
     for (int g = g0; g < g1; ++g) {
@@ -345,7 +347,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
         float ap[kVecs];
 #pragma unroll
         for (int v = 0; v < kVecs; ++v) ap[v] = act_par[g * MV + min(kVecs * t + v, MV - 1)];
-        if (kInAct && g == g0) __syncwarp();  // all lanes have read what the sums replace
+        if (IN_ACT && g == g0) __syncwarp();  // all lanes have read what the sums replace
         const uint8_t* row = smem + r * pitch + t * 16 + g * 64;
         const __nv_bfloat16* sc = scl + r * c.share + g;
         float* out = sums + r * MV + kVecs * t;
@@ -417,7 +419,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
         for (; q + 2 <= nt * PARTS; q += 2) tiles(q, std::integral_constant<int, 2>{});
         if (q < nt * PARTS) tiles(q, std::integral_constant<int, 1>{});
     }
-    if (!kInAct && g0 == g1)  // no group: nothing of this warp's, but its copies
+    if (!IN_ACT && g0 == g1)  // no group: nothing of this warp's, but its copies
         for (int i = lane; i < outs * PARTS; i += 32) sums[i] = 0.f;
     for (int q = 0; q < nt * PARTS; ++q)
         if (g0 == g1 && !mbar_arrived(&bars[q])) late = 1;
@@ -441,7 +443,7 @@ __global__ void __launch_bounds__(max_warps(MV) * 32, 1) gemv_w4_kernel(const W4
         for (int w = 0; w < W; ++w) {
 #pragma unroll
             for (int h = 0; h < PARTS; ++h)
-                if (!kInAct) {
+                if (!IN_ACT) {
                     v[h] += all[(size_t)w * outs * PARTS + first + h * 16 * MV];
                 } else {  // where warp w's first group was, if it had any
                     const int from = first_of(w), to = first_of(w + 1);
@@ -484,12 +486,12 @@ constexpr size_t kBlockSmem = 227 * 1024 - 1024;  // the barriers' share left ou
 
 // Blocks, warps a block, tiles a block and the split of K for p at MV vectors;
 // at_once[i]: clusters of 2^i blocks of this kernel that run at once.
-W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, const int at_once[4]) {
-    const int groups = p.K / kW4Group, ntiles = (p.N + 15) / 16;
+W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, bool in_act, const int at_once[4]) {
+    const int groups = p.K / kW4Group, ntiles = (p.N + 15) / 16, most_tiles = in_act ? kMaxTiles / 2 : kMaxTiles;
     auto made = [&](int log_split, int tiles, int grid) {
         const int share = (groups + (1 << log_split) - 1) >> log_split, warps = std::min(share, max_warps(mv));
         return W4Launch{warps, tiles, share, log_split, grid, ((1ull << 32) + warps - 1) / warps,
-                        smem_of(mv, parts, tiles, share, warps).total};
+                        smem_of(mv, parts, in_act, tiles, share, warps).total};
     };
     // All tiles resident at once, a block an SM, K split so that the estimate is
     // least: a warp's turns (groups of K, between the most a warp has and the mean)
@@ -504,7 +506,7 @@ W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, const int at_once[4]
     float least = 0.f;
     for (int ls = 0; ls < end; ++ls) {
         const int most = std::max(1, std::min(ntiles, at_once[ls])), tiles = (ntiles + most - 1) / most;
-        if (tiles > (sums_in_act(mv, parts) ? kMaxTiles / 2 : kMaxTiles)) continue;
+        if (tiles > most_tiles) continue;
         const W4Launch c = made(ls, tiles, most);
         if (c.smem > kBlockSmem) continue;
         const float turns = 0.5f * ((float)((c.share + c.warps - 1) / c.warps) + (float)c.share / (float)c.warps);
@@ -517,39 +519,63 @@ W4Launch plan_gemv_w4(const W4Params& p, int mv, int parts, const int at_once[4]
     if (best.warps) return best;
     // more tiles than that: as many a block as fit, over several rounds of blocks
     for (int ls = 0; ls < end; ++ls)
-        for (int tiles = std::min(sums_in_act(mv, parts) ? kMaxTiles / 2 : kMaxTiles, ntiles); tiles >= 1; --tiles) {
+        for (int tiles = std::min(most_tiles, ntiles); tiles >= 1; --tiles) {
             const W4Launch c = made(ls, tiles, (ntiles + tiles - 1) / tiles);
             if (c.smem <= kBlockSmem && (tiles >= 2 || ls == end - 1)) return c;
         }
     return W4Launch{};
 }
+// How often all SMs take a block.
+inline int rounds_of(const W4Launch& c, const int at_once[4]) {
+    const int most = std::max(1, at_once[c.log_split]);
+    return (c.grid + most - 1) / most;
+}
+// Whether the plan with the sums in the activations' place saves a round of blocks.
+inline bool saves_a_round(const W4Launch& in_act, const W4Launch& own, const int at_once[4]) {
+    return in_act.warps && (!own.warps || rounds_of(in_act, at_once) < rounds_of(own, at_once));
+}
+
+// How many clusters of 1, 2, 4 and 8 blocks of a kernel run at once with a block an SM,
+// the kernel's shared-memory limit raised; once per device.
+template <int MV, int PARTS, bool IN_ACT>
+cudaError_t prepare_gemv_w4(int dev, int sms, int at_once[4]) {
+    static std::mutex mu;
+    static int at_once_of[64][4] = {};
+    const auto kern = gemv_w4_kernel<MV, PARTS, IN_ACT>;
+    const std::lock_guard<std::mutex> lock(mu);
+    int* v = at_once_of[dev & 63];
+    if (!v[0]) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBlockSmem);
+        if (e != cudaSuccess) return e;
+        int n[4] = {sms, 0, 0, 0};
+        for (int ls = 1; ls < 4; ++ls) {
+            e = clusters_at_once(kern, max_warps(MV) * 32, kBlockSmem, 1, 1 << ls, &n[ls]);
+            if (e != cudaSuccess) return e;
+        }
+        std::copy(n, n + 4, v);
+    }
+    std::copy(v, v + 4, at_once);
+    return cudaSuccess;
+}
 
 template <int MV, int PARTS>
 cudaError_t launch_gemv_w4_as(const W4Params& p, int dev, int sms, cudaStream_t s) {
-    // per device: the shared-memory limit raised, and how many clusters of 1, 2, 4
-    // and 8 blocks run at once with a block an SM
-    static std::mutex mu;
-    static int at_once_of[64][4] = {};
-    const auto kern = gemv_w4_kernel<MV, PARTS>;
     int at_once[4];
-    {
-        const std::lock_guard<std::mutex> lock(mu);
-        int* v = at_once_of[dev & 63];
-        if (!v[0]) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kBlockSmem);
-            if (e != cudaSuccess) return e;
-            int n[4] = {sms, 0, 0, 0};
-            for (int ls = 1; ls < 4; ++ls) {
-                e = clusters_at_once(kern, max_warps(MV) * 32, kBlockSmem, 1, 1 << ls, &n[ls]);
-                if (e != cudaSuccess) return e;
-            }
-            std::copy(n, n + 4, v);
-        }
-        std::copy(v, v + 4, at_once);
+    cudaError_t e = prepare_gemv_w4<MV, PARTS, false>(dev, sms, at_once);
+    if (e != cudaSuccess) return e;
+    const W4Launch c = plan_gemv_w4(p, MV, PARTS, false, at_once);
+    if constexpr (has_in_act(MV, PARTS)) {
+        int at_once_in[4];
+        e = prepare_gemv_w4<MV, PARTS, true>(dev, sms, at_once_in);
+        if (e != cudaSuccess) return e;
+        const W4Launch in = plan_gemv_w4(p, MV, PARTS, true, at_once_in);
+        if (saves_a_round(in, c, at_once))
+            return launch_ordered(gemv_w4_kernel<MV, PARTS, true>, dim3(in.grid, 1, 1 << in.log_split), dim3(in.warps * 32),
+                                  in.smem, s, 1, 1 << in.log_split, p, in);
     }
-    const W4Launch c = plan_gemv_w4(p, MV, PARTS, at_once);
     if (!c.warps) return cudaErrorInvalidValue;
-    return launch_ordered(kern, dim3(c.grid, 1, 1 << c.log_split), dim3(c.warps * 32), c.smem, s, 1, 1 << c.log_split, p, c);
+    return launch_ordered(gemv_w4_kernel<MV, PARTS, false>, dim3(c.grid, 1, 1 << c.log_split), dim3(c.warps * 32), c.smem, s,
+                          1, 1 << c.log_split, p, c);
 }
 
 cudaError_t launch_gemv_w4(const W4Params& p, int dev, int sms, cudaStream_t s) {

@@ -290,3 +290,22 @@ def test_calls_from_two_threads(ads):
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert not wrong
+
+
+@pytest.mark.parametrize("M", [3, 4])
+@pytest.mark.parametrize("N,K,norm", [(9728, 2560, True), (16384, 2560, False), (6144, 2560, True), (4096, 2048, True), (500, 12288, False), (1152, 512, True)])
+def test_gemv_w4_gate_up_of_four_vectors_in_both_forms(ads, M, N, K, norm):
+    """The sums in a place of their own, or where a warp's first activations were."""
+    import torch
+    b, s = weights(2 * N, K, 47)
+    x = synth.normal_f32(5, 48 + M, (M, K), std=1.5)
+    gamma = synth.normal_bf16(3, 49, (K,), std=0.02, mean=1.0) if norm else None
+    want, tol = ref.gemv_w4(x, b, s, 2, None, gamma)
+    pad = torch.full((M * N + 64,), 7.25, device="cuda")
+    y = pad[32:32 + M * N].view(M, N)
+    args = (dev(x), dev(b), dev(s), y, 2, None, None if gamma is None else dev(gamma))
+    ads.gemv_w4(*args)
+    near(y.cpu().numpy(), want, tol)
+    first = y.clone()
+    ads.gemv_w4(*args)
+    assert torch.equal(first, y) and (pad[:32] == 7.25).all() and (pad[32 + M * N:] == 7.25).all()
