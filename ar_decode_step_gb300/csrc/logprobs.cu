@@ -32,8 +32,10 @@ constexpr int kRun = 32 * kRunNv;
 constexpr int kShortWarps = 4;
 constexpr int kLongWarps = 16;            // warps a block, at most, long rows
 // Up to so many alternatives the lanes' maxima are taken one by one to find the
-// bound, above it by halving (4096 frames x 8 x 1026: 8 alternatives 32.0 us one by
-// one, 30.9 by halving; 3 28.4 and 29.5).
+// bound, above it by halving (one by one and by halving, us: 4096 frames x 8 x 1026 with
+// 3 alternatives 28.4 and 29.0, 4 28.6 and 29.0, 5 29.6 and 29.7, 6 31.1 and 30.2, 8 32.4
+// and 30.8; 40 frames 5 2.9 and 3.0, 8 3.3 and 3.1; 512 x 32000 5 19.7 and 19.8, 6 20.4 and
+// 20.3, 16 26.9 and 23.6).
 constexpr int kOneByOne = 5;
 
 __device__ __forceinline__ float ex2(float x) {

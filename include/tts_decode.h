@@ -447,9 +447,15 @@ int tts_dequantize_kv4(const void* k4, const void* v4, const void* k_par, const 
  * value (those of pos too) as the cache holds it.  qkv, q_norm, k_norm, out,
  * head counts as tts_attention_decode; max_pos up to 2^20, n_q up to 4096,
  * n_kv up to 1024.
- * Scores, softmax and sums are fp32, the new key is computed to about 2^-44 up
- * to its rounding (its codes do not depend on the order of a sum), and every
- * result is deterministic.  kv_row: DEVICE fp32 [2][n_kv][128], the key and
+ * Codes are exact operands; queries, and weights times value scales, take part
+ * with 22 bits, as two fp16 numbers under a power of two (to no less than 2^-39
+ * of the largest of a query, 2^-33 of the largest weight so far).  Sums, maxima and
+ * the join of partial results are fp32, exponentials the hardware's base-2 ones
+ * (2 ulp): together as exact as fp32 on the cache's values.  The new key is
+ * computed to about 2^-44, its angles in fp64, up to its rounding (its codes do
+ * not depend on the order of a sum).  Squares are summed in fp32: |qkv| below
+ * 2^60, and with an eps of 0 the largest of each head above 2^-40.  Results do
+ * not depend on the run.  kv_row: DEVICE fp32 [2][n_kv][128], the key and
  * value of pos as the cache now holds them, or NULL.
  * workspace: DEVICE, at least tts_attention_kv4_workspace bytes, 16-byte
  * aligned, zeroed once by the caller before its first use; every call leaves
@@ -480,7 +486,8 @@ int tts_attention_decode_kv4(const float* qkv, const void* q_norm, const void* k
  * Entries of -inf (masked) have probability 0 and no share in the entropy; a
  * codebook with nothing but -inf has log probabilities -inf and entropy 0.
  * With a NaN or +inf among its logits a codebook's log probabilities and
- * entropy are NaN; NaN entries rank last.  DEVICE outputs, fp32 and int32.
+ * entropy are NaN; NaN entries rank last.  Sums are fp32, exponentials the
+ * hardware's base-2 ones (2 ulp).  DEVICE outputs, fp32 and int32.
  * 0 <= rows (0: nothing is done, pointers may be NULL), 1 <= n_cb <= 8,
  * 2 <= cb_vocab <= 2^20, 0 <= top <= min(32, cb_vocab), temperature finite and
  * at least 2^-126.  Pointers 4-byte aligned; outputs overlap neither the logits (from
