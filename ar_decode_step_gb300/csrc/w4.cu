@@ -119,7 +119,7 @@ __host__ __device__ constexpr int act_group_bytes(int mv) { return 4 * columns_o
 // a place of their own, or (in_act) where its first group's activations were, which
 // are in registers by then.  The second is 5 to 17 % slower at equal plans (gate/up
 // 6144 x 2560 8.2 us against 7.7, 4096 x 2048 5.9 and 5.5, 2560 x 9728 20.7 and 17.4)
-// and saves 21 KB a block for four tiles: it is taken where that saves a round of
+// and saves 41 KB a block of four tiles: it is taken where that saves a round of
 // blocks (9728 x 2560 10.2 against 14.7, 16384 x 2560 19.0 and 22.1).  Elsewhere a
 // round is not to be had.
 __host__ __device__ constexpr bool has_in_act(int mv, int parts) { return mv == 4 && parts == 2; }
