@@ -575,7 +575,12 @@ class Decoder:
         n = self.dims.n_cb
         lp, ent = np.empty(n, np.float32), np.empty(n, np.float32)
         at, at_lp = np.empty((n, max(top, 0)), np.int32), np.empty((n, max(top, 0)), np.float32)
-        c = None if codes is None else np.ascontiguousarray(codes, np.int32).reshape(n)
+        c = None
+        if codes is not None:
+            c = np.asarray(codes).reshape(n)
+            if not ((c >= 0) & (c < self.dims.cb_vocab)).all():  # before a wider integer wraps
+                raise TtsError("tts_get_logprobs", -2)
+            c = np.ascontiguousarray(c, np.int32)
         _call("tts_get_logprobs", self._ctx, None if c is None else _ptr(c), float(temperature), top, _ptr(lp),
               _ptr(ent), _ptr(at) if top > 0 else None, _ptr(at_lp) if top > 0 else None)
         return lp, ent, at, at_lp

@@ -160,3 +160,21 @@ def test_code_logprobs_takes_temperatures_that_are_normal_numbers(lib):
         assert lib.tts_code_logprobs(*dict(none, T=T).values()) == 0
     for T in (1.1e-38, 6e-39, 1e-45, -1e-37):
         assert lib.tts_code_logprobs(*dict(none, T=T).values()) == ARG, T
+
+
+def test_decoder_logprobs_refuses_codes_that_wrap(lib):
+    """A code of 2^32 + 5 is not code 5 (found before the context is looked at)."""
+    import numpy as np
+    import ar_decode_step_gb300 as m
+    dec = object.__new__(m.Decoder)
+    dec._ctx, dec.dims = None, m.Dims()
+    n, V = dec.dims.n_cb, dec.dims.cb_vocab
+    for bad in (2 ** 32 + 5, -2 ** 32, V, -1, float("nan")):
+        codes = np.zeros(n, np.float64 if bad != bad else np.int64)
+        codes[n - 1] = bad
+        with pytest.raises(m.TtsError) as e:
+            dec.logprobs(codes)
+        assert e.value.status == -2, bad
+    with pytest.raises(m.TtsError) as e:
+        dec.logprobs(np.full(n, V - 1))
+    assert e.value.status == -6  # codes in range: the context is what is missing
