@@ -454,8 +454,9 @@ int tts_dequantize_kv4(const void* k4, const void* v4, const void* k_par, const 
  * (2 ulp): together as exact as fp32 on the cache's values.  The new key is
  * computed to about 2^-44, its angles in fp64, up to its rounding (its codes do
  * not depend on the order of a sum).  Squares are summed in fp32: |qkv| below
- * 2^60, and with an eps of 0 the largest of each head above 2^-40.  Results do
- * not depend on the run.  kv_row: DEVICE fp32 [2][n_kv][128], the key and
+ * 2^60, and with an eps of 0 the largest of each head above 2^-40; cached values
+ * up to 2^100 (weights of up to 2^8 times them are added over the positions).
+ * Results do not depend on the run.  kv_row: DEVICE fp32 [2][n_kv][128], the key and
  * value of pos as the cache now holds them, or NULL.
  * workspace: DEVICE, at least tts_attention_kv4_workspace bytes, 16-byte
  * aligned, zeroed once by the caller before its first use; every call leaves
