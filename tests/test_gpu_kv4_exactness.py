@@ -61,3 +61,22 @@ def test_one_position_holds_the_weight(ads, n_q, n_kv, pos):
 def _like(x):
     import torch
     return torch.from_numpy(x.view(np.int16) if x.dtype == np.uint16 else x).cuda()
+
+
+@pytest.mark.parametrize("n_q,n_kv,pos", [(8, 2, 20), (8, 2, 700), (4, 1, 9000), (16, 2, 3000)])
+@pytest.mark.parametrize("scale", [2.0 ** 98, 2.0 ** -100])
+def test_values_of_extreme_size(ads, n_q, n_kv, pos, scale):
+    """Value rows next to the largest and far below one: as exact as ordinary ones."""
+    import four_bit_ref as ref
+    import synth
+    k4, kp, _, _ = cache(n_kv, pos + 2, 140)
+    v = synth.normal_f32(1, 141, (n_kv, pos + 2, 128)).astype(np.float64) * scale
+    v4, vp = ref.quant_kv4(ref.bf16_bits(v.astype(np.float32)))
+    a = Attn(ads, n_q, n_kv, pos + 2, pos, arrays=(k4, kp, v4, vp))
+    a.qkv[(n_q + n_kv) * 128:] *= np.float32(scale)
+    a.d[0].copy_(_like(a.qkv))
+    a.call()
+    a.check()
+    want, limit = kx.judged(a.qkv, a.qn, a.kn, a.k4, a.kp, a.v4, a.vp, n_q, n_kv, pos)
+    got = kx.off(host(a.out), want)
+    assert got <= limit, (got, limit)
